@@ -21,8 +21,8 @@
  * The output of a step is read after its own token is applied: y_t = S_t^T q_t.
  *
  * General conventions (every call):
- *  - All tensors are fp32, C-contiguous, device memory owned by the caller, and
- *    16-byte aligned (else SKETCHSSM_ERR_ALIGNMENT).  A pointer that is not device
+ *  - All tensors are fp32 and C-contiguous (but for what a call says otherwise), device
+ *    memory owned by the caller, and 16-byte aligned (else SKETCHSSM_ERR_ALIGNMENT).  A pointer that is not device
  *    accessible (plain host memory) is rejected with SKETCHSSM_ERR_INVALID_ARG.
  *  - Layouts (B batch rows, H state heads, Hqk q/k heads, G basis groups, Rb basis
  *    rows per group, W window, Rtot = sum of the sketch heads' ranks):
@@ -319,6 +319,97 @@ sketchssm_status sketchssm_step(const sketchssm_plan *plan, const float *q, cons
 sketchssm_status sketchssm_prefill(const sketchssm_plan *plan, int32_t T, const float *k, const float *v,
                                    const float *a, const float *beta, float *S, const float *omega,
                                    float *Y, sketchssm_stream stream);
+
+/* ---- the gated delta rule on packed tokens, and the norm behind it ----
+ *
+ * The calls above keep fp32 tokens, one per batch row.  The three calls below serve the
+ * layer around them: prompts of different lengths with their outputs, tokens of 16-bit
+ * types, states that rows address by slot, and the gated norm that a layer's read passes
+ * before the output projection.  States stay fp32, S [B][H][K][V] of the plan, so prompts,
+ * single tokens, sketch decodes and flushes take turns on them.
+ */
+
+/* Types of token tensors. */
+typedef enum {
+    SKETCHSSM_F32 = 0,
+    SKETCHSSM_BF16 = 1,
+    SKETCHSSM_F16 = 2
+} sketchssm_dtype;
+
+/* The token tensors q [N][Hqk][K], k [N][Hqk][K], v [N][H][V], y [N][H][V]: their type, the
+ * elements between two tokens (0: packed; else at least the token's own, a multiple of 16
+ * bytes), and what is done to q and k. */
+typedef struct {
+    int32_t dtype;        /* sketchssm_dtype of q, k, v and y */
+    int32_t normalize_qk; /* nonzero: q and k are brought to unit length, x / sqrt(sum x^2 + 1e-6) */
+    float scale;          /* factor on q (1: none) */
+    int64_t q_stride, k_stride, v_stride, y_stride;
+} sketchssm_token_desc;
+
+/*
+ * The gated delta rule, chunked: `seqs` sequences packed one behind the other.  Sequence i
+ * holds the tokens cu[i] .. cu[i+1]-1 of the `tokens` there are and continues the state of
+ * slot[i]: for each of its tokens, in order, and every head
+ *     S <- a (I - beta k k^T) S + beta k v^T,     y = S^T q   (after the update)
+ * S [B][H][K][V] fp32 is updated in place.  To start from nothing, zero the slot first.
+ *  - The plan's kind is SKETCHSSM_GDN (others: SKETCHSSM_ERR_UNSUPPORTED); its rank table,
+ *    window and buffers are not used.  A sketch is formed with sketchssm_flush(n_tokens = 0)
+ *    afterwards; that leaves the sketches of other rows what they were.
+ *  - cu [seqs+1] and slot [seqs] are int32 on the device; slot NULL: sequence i has state i
+ *    (then seqs <= B).  a, beta [tokens][H] fp32, a in [0, 1].  q, k, v, y as td says; y
+ *    overlaps no input.
+ *  - An empty sequence, or one whose slot is negative (padding), is skipped: its state and
+ *    its rows of y stay as they were, as do rows of y that no sequence holds.
+ *  - Slots differ.  A sequence whose slot is >= B or is named by an earlier one too, or
+ *    whose bounds are not 0 <= cu[i] <= cu[i+1] <= tokens, is skipped, and
+ *    sketchssm_plan_check reports SKETCHSSM_ERR_INVALID_ARG.
+ *  - Sums and the state are fp32 (or exact splits of fp32); y is rounded once.
+ *  - seqs = 0 and tokens = 0 do nothing.  Nothing is allocated; the call can be captured
+ *    into a graph.
+ */
+sketchssm_status sketchssm_delta_chunk(const sketchssm_plan *plan, const sketchssm_token_desc *td, int32_t seqs,
+                                       int32_t tokens, const int32_t *cu, const int32_t *slot, const void *q,
+                                       const void *k, const void *v, const float *a, const float *beta, float *S,
+                                       void *y, sketchssm_stream stream);
+
+/*
+ * The gated delta rule, recurrent: one token for each of `rows` rows, row i on the state of
+ * slot[i].  Equal to sketchssm_delta_chunk with cu = 0, 1, .., rows, and bound by the same
+ * rules; beside sketchssm_step it takes 16-bit tokens, strided tensors and slots.
+ */
+sketchssm_status sketchssm_delta_step(const sketchssm_plan *plan, const sketchssm_token_desc *td, int32_t rows,
+                                      const int32_t *slot, const void *q, const void *k, const void *v,
+                                      const float *a, const float *beta, float *S, void *y,
+                                      sketchssm_stream stream);
+
+/* Gates of sketchssm_gated_norm. */
+typedef enum {
+    SKETCHSSM_SILU = 0,   /* z / (1 + exp(-z)) */
+    SKETCHSSM_SIGMOID = 1 /* 1 / (1 + exp(-z)) */
+} sketchssm_gate;
+
+/* Shape of a gated norm: x, z, out [rows][groups][width], weight [weight_groups][width]. */
+typedef struct {
+    int32_t x_dtype;       /* sketchssm_dtype of x */
+    int32_t dtype;         /* sketchssm_dtype of z and out */
+    int32_t groups;        /* groups of a row, each normalised by itself */
+    int32_t width;         /* values of a group: a multiple of 8 up to 16384 */
+    int32_t weight_groups; /* 1: one weight for all groups; groups: one each */
+    int32_t gate;          /* sketchssm_gate */
+    int32_t gate_first;    /* 0: out = norm(x) w gate(z); else out = norm(x gate(z)) w */
+    float eps;
+    int64_t x_stride, z_stride, out_stride; /* elements between rows (0: packed; a multiple of 16 bytes) */
+} sketchssm_norm_desc;
+
+/*
+ * The gated norm behind a layer's read: norm(x) = x / sqrt(mean of x^2 over the group + eps),
+ * times the fp32 weight and the gate of z.  Gated DeltaNet: groups = H, width = V, the gate
+ * after the norm; Mamba-2: groups = G, width = H V / G, the gate first, a weight a group.
+ * z NULL: no gate.  Sums and products are fp32, out is rounded once.  out may be x or z
+ * themselves where type and stride agree, and overlaps them in no other way.
+ */
+sketchssm_status sketchssm_gated_norm(const sketchssm_norm_desc *nd, int32_t rows, const void *x, const void *z,
+                                      const float *weight, void *out, sketchssm_stream stream);
 
 /* Static text of a status code. */
 const char *sketchssm_status_string(sketchssm_status status);

@@ -16,22 +16,35 @@ One layer at batch B (tensors fp32 on the GPU; layouts in include/sketchssm.h)::
         y = layer.decode(t % 16, q, k, v, a)   # never reads S for sketch heads
         if t % 16 == 15:
             layer.flush(16)              # the buffered tokens reach S; Y is re-formed
+
+A Gated DeltaNet layer in a server: packed prompts of different lengths with their outputs,
+single tokens on states addressed by slot, and the gated norm before the output projection::
+
+    y = layer.prompt(cu, q_p, k_p, v_p, a_p, beta_p, slot=slots)   # bf16, S and sketches updated
+    y = layer.step(q, k, v, a, beta, slot=rows, gate=z)            # y normed and gated
 """
 from ._binding import (  # noqa: F401
     DENSE,
+    DTYPES,
     EXPORTS,
+    GATES,
     KINDS,
     LIB_PATH,
     Desc,
+    NormDesc,
     Plan,
     SketchSSMError,
+    TokenDesc,
     load,
     sketchssm_decode,
     sketchssm_decode_rows,
     sketchssm_decode_static_scratch,
+    sketchssm_delta_chunk,
+    sketchssm_delta_step,
     sketchssm_dense_decode,
     sketchssm_flush,
     sketchssm_flush_rows,
+    sketchssm_gated_norm,
     sketchssm_plan_create,
     sketchssm_plan_destroy,
     sketchssm_prefill,

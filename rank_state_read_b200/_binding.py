@@ -24,7 +24,13 @@ STATUS = {0: "SKETCHSSM_OK", 1: "SKETCHSSM_ERR_INVALID_ARG", 2: "SKETCHSSM_ERR_A
 EXPORTS = ("sketchssm_plan_create", "sketchssm_plan_query", "sketchssm_plan_check",
            "sketchssm_plan_set_wait_limit", "sketchssm_plan_destroy", "sketchssm_flush", "sketchssm_decode", "sketchssm_dense_decode",
            "sketchssm_decode_static_scratch", "sketchssm_step", "sketchssm_decode_rows",
-           "sketchssm_flush_rows", "sketchssm_prefill", "sketchssm_status_string", "sketchssm_last_error")
+           "sketchssm_flush_rows", "sketchssm_prefill", "sketchssm_status_string", "sketchssm_last_error",
+           "sketchssm_delta_chunk", "sketchssm_delta_step", "sketchssm_gated_norm")
+
+
+# sketchssm_dtype, sketchssm_gate
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+GATES = {"silu": 0, "sigmoid": 1}
 
 
 class SketchSSMError(RuntimeError):
@@ -37,6 +43,21 @@ class Desc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in
                 ("kind", "batch", "heads", "qk_heads", "key_dim", "value_dim", "window", "groups",
                  "basis_rows", "rank_cap")]
+
+
+class TokenDesc(ctypes.Structure):
+    """sketchssm_token_desc"""
+    _fields_ = [("dtype", ctypes.c_int32), ("normalize_qk", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    """sketchssm_norm_desc"""
+    _fields_ = [(f, ctypes.c_int32) for f in
+                ("x_dtype", "dtype", "groups", "width", "weight_groups", "gate", "gate_first")] + [
+                    ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                    ("out_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -65,7 +86,10 @@ def load():
     lib.sketchssm_decode_rows.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P]
     lib.sketchssm_flush_rows.argtypes = [P, P, P, P, P, P, P, P, P, P]
     lib.sketchssm_prefill.argtypes = [P, I32, P, P, P, P, P, P, P, P]
-    for f in EXPORTS[:13]:
+    lib.sketchssm_delta_chunk.argtypes = [P, ctypes.POINTER(TokenDesc), I32, I32, P, P, P, P, P, P, P, P, P, P]
+    lib.sketchssm_delta_step.argtypes = [P, ctypes.POINTER(TokenDesc), I32, P, P, P, P, P, P, P, P, P]
+    lib.sketchssm_gated_norm.argtypes = [ctypes.POINTER(NormDesc), I32, P, P, P, P, P]
+    for f in EXPORTS[:13] + EXPORTS[15:]:
         getattr(lib, f).restype = ctypes.c_int
     lib.sketchssm_status_string.argtypes = [ctypes.c_int]
     lib.sketchssm_status_string.restype = ctypes.c_char_p
@@ -288,3 +312,102 @@ def sketchssm_flush_rows(plan: Plan, S, omega, kbuf, vbuf, abuf, bbuf, n_tokens,
         _ptr(vbuf, "vbuf", n("vbuf")), _ptr(abuf, "abuf", n("abuf")), _ptr(bbuf, "bbuf", n("bbuf")),
         _rows(n_tokens, "n_tokens", plan.desc.batch), _ptr(Y, "Y", n("Y")), _stream(stream)),
         "sketchssm_flush_rows")
+
+
+def _rows3(t, name: str, dtype, n: int, inner: int):
+    """Pointer and row stride of a tensor [n][x][y] whose rows are contiguous (x y = inner)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] * t.shape[2] != inner:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} rows of {inner} values in three dimensions")
+    if n == 0:
+        return None, 0
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and t.shape[2] != 1) or (s1 != t.shape[2] and t.shape[1] != 1):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if n == 1:
+        return t.data_ptr(), 0
+    if s0 < inner:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), s0
+
+
+def _ints(t, name: str, numel: int):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    return t.data_ptr()
+
+
+def _delta(plan: Plan, n: int, q, k, v, a, beta, S, y, normalize_qk, scale):
+    d = plan.desc
+    H, qk, hv = d.heads, d.qk_heads * d.key_dim, d.heads * d.value_dim
+    dtype = getattr(q, "dtype", None)
+    if dtype not in DTYPES:
+        raise TypeError(f"q must be a float32, bfloat16 or float16 tensor, got {dtype}")
+    qp, qs = _rows3(q, "q", dtype, n, qk)
+    kp, ks = _rows3(k, "k", dtype, n, qk)
+    vp, vs = _rows3(v, "v", dtype, n, hv)
+    yp, ys = _rows3(y, "y", dtype, n, hv)
+    td = TokenDesc(DTYPES[dtype], bool(normalize_qk), scale, qs, ks, vs, ys)
+    return td, (qp, kp, vp, _ptr(a, "a", n * H), _ptr(beta, "beta", n * H), _ptr(S, "S", plan.numel("S")), yp)
+
+
+def sketchssm_delta_chunk(plan: Plan, cu, q, k, v, a, beta, S, y, *, slot=None, normalize_qk: bool = False,
+                          scale: float = 1.0, stream=None) -> None:
+    """The gated delta rule on packed prompts (sketchssm_delta_chunk): sequence i holds the tokens
+    cu[i] .. cu[i+1]-1 and continues state slot[i] (None: state i) of S in place; y gets the
+    tokens' outputs.  cu [seqs+1], slot [seqs]: int32 on the device; q, k [N][Hqk][K], v, y
+    [N][H][V] of one type (fp32, bf16, fp16), contiguous but for the stride between tokens; a,
+    beta [N][H] fp32.  With ``normalize_qk`` q and k are brought to unit length first; ``scale``
+    multiplies q."""
+    if not isinstance(cu, torch.Tensor) or cu.numel() < 1:
+        raise TypeError("cu must be an int32 CUDA tensor of one entry more than there are sequences")
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    n, seqs = q.shape[0], cu.numel() - 1
+    td, ptrs = _delta(plan, n, q, k, v, a, beta, S, y, normalize_qk, scale)
+    _check(load().sketchssm_delta_chunk(plan.handle, td, seqs, n, _ints(cu, "cu", seqs + 1),
+                                        _ints(slot, "slot", seqs), *ptrs, _stream(stream)), "sketchssm_delta_chunk")
+
+
+def sketchssm_delta_step(plan: Plan, q, k, v, a, beta, S, y, *, slot=None, normalize_qk: bool = False,
+                         scale: float = 1.0, stream=None) -> None:
+    """The gated delta rule on one token a row (sketchssm_delta_step): row i on state slot[i] (None:
+    state i).  Tensors as for sketchssm_delta_chunk."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    n = q.shape[0]
+    td, ptrs = _delta(plan, n, q, k, v, a, beta, S, y, normalize_qk, scale)
+    _check(load().sketchssm_delta_step(plan.handle, td, n, _ints(slot, "slot", n), *ptrs, _stream(stream)),
+           "sketchssm_delta_step")
+
+
+def sketchssm_gated_norm(x, z, weight, out, *, eps: float = 1e-6, activation: str = "silu",
+                         gate_first: bool = False, stream=None) -> None:
+    """The gated norm behind a layer's read (sketchssm_gated_norm): RMS norm of x [rows][groups][width]
+    over each group, times weight ([width], or [groups][width]) and the gate of z (None: no gate),
+    which multiplies after the norm or, with ``gate_first``, before it.  x, z, out may be strided
+    between rows; out has z's type (without z: its own) and may be x or z itself."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.dtype not in DTYPES:
+        raise TypeError("x must be a float32, bfloat16 or float16 tensor [rows][groups][width]")
+    if not isinstance(out, torch.Tensor) or out.dtype not in DTYPES:
+        raise TypeError("out must be a float32, bfloat16 or float16 tensor")
+    if activation not in GATES:
+        raise ValueError(f"activation must be one of {sorted(GATES)}, got {activation!r}")
+    n, groups, width = x.shape
+    xp, xs = _rows3(x, "x", x.dtype, n, groups * width)
+    zp, zs = (None, 0) if z is None else _rows3(z, "z", out.dtype, n, groups * width)
+    op, os_ = _rows3(out, "out", out.dtype, n, groups * width)
+    wg = 1 if isinstance(weight, torch.Tensor) and weight.numel() == width else groups
+    nd = NormDesc(DTYPES[x.dtype], DTYPES[out.dtype], groups, width, wg, GATES[activation], bool(gate_first), eps,
+                  xs, zs, os_)
+    _check(load().sketchssm_gated_norm(nd, n, xp, zp, _ptr(weight, "weight", wg * width), op, _stream(stream)),
+           "sketchssm_gated_norm")

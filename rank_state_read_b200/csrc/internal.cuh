@@ -115,6 +115,38 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 bool prefill_tcgen05_fits(const PrefillArgs &a);
 cudaError_t launch_prefill_tcgen05(const PrefillArgs &a, cudaStream_t stream);
 
+// The gated delta rule on packed tokens (row = sequence).  cu [rows + 1] gives each row's
+// tokens, or null: row r is token r.  slot [rows] gives each row's state, or null: state r.
+constexpr float DELTA_QK_EPS = 1e-6f;
+struct DeltaArgs {
+    int dtype, rows, tokens, slots, H, Hqk, V, hpq;
+    int VS;  // column slab of one CTA of the token-by-token kernel (step_slab)
+    int normalize;
+    float scale;
+    long long q_stride, k_stride, v_stride, y_stride;  // elements between tokens
+    const int *cu, *slot;
+    const void *q, *k, *v;
+    const float *a, *beta;
+    float *S;
+    void *y;
+    int *status;
+    long long wait_limit;
+};
+cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t stream);
+
+// The gated norm: `items` = rows x groups, each of `width` values.
+constexpr int NORM_MAX_WIDTH = 16384;
+struct NormArgs {
+    int x_dtype, dtype, groups, width, weight_groups;
+    int sigmoid, gate_first;
+    float eps;
+    long long items, x_stride, z_stride, out_stride;
+    const void *x, *z;
+    const float *weight;
+    void *out;
+};
+cudaError_t launch_gated_norm(const NormArgs &a, cudaStream_t stream);
+
 int flush_slab(int V);
 size_t flush_smem_bytes(int kind, int V, int W, int rcap);
 cudaError_t launch_flush(const FlushArgs &a, cudaStream_t stream);

@@ -47,14 +47,14 @@ AddrRangeFn addr_range_fn()
 
 // A tensor argument must be 16-byte aligned device memory (of the current device,
 // or managed / mapped host memory) whose allocation holds `bytes` from `p` on.
-sketchssm_status check_tensor(const void *p, size_t bytes, const char *name, bool may_be_null)
+sketchssm_status check_tensor(const void *p, size_t bytes, const char *name, bool may_be_null, int align = 16)
 {
     if (p == nullptr) {
         if (may_be_null || bytes == 0) return SKETCHSSM_OK;
         return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " is NULL");
     }
-    if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
-        return fail(SKETCHSSM_ERR_ALIGNMENT, std::string(name) + " is not 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(p) % align != 0)
+        return fail(SKETCHSSM_ERR_ALIGNMENT, std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
     cudaPointerAttributes at;
     cudaError_t e = cudaPointerGetAttributes(&at, p);
     if (e != cudaSuccess) {
@@ -88,6 +88,13 @@ sketchssm_status check_tensor(const void *p, size_t bytes, const char *name, boo
     do {                                                                       \
         sketchssm_status s_ = check_tensor((ptr), (bytes), (name), (nullable)); \
         if (s_ != SKETCHSSM_OK) return s_;                                     \
+    } while (0)
+
+// A tensor read one 4-byte value at a time.
+#define CHECK_I(ptr, bytes, name, nullable)                                       \
+    do {                                                                          \
+        sketchssm_status s_ = check_tensor((ptr), (bytes), (name), (nullable), 4); \
+        if (s_ != SKETCHSSM_OK) return s_;                                        \
     } while (0)
 
 sketchssm_status check_desc(const sketchssm_desc *d)
@@ -727,5 +734,165 @@ extern "C" sketchssm_status sketchssm_step(const sketchssm_plan *p, const float 
     A.y = y;
     cudaError_t e = sk::launch_step(A, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "standard step kernel launch");
+    return SKETCHSSM_OK;
+}
+
+namespace {
+
+int dtype_size(int dtype) { return dtype == SKETCHSSM_F32 ? 4 : 2; }
+
+// Resolves a stride (0: packed) of `elems` values a row and checks that vectors of 16
+// bytes stay aligned; `bytes` gets what `rows` rows span.
+sketchssm_status row_span(long long &stride, long long elems, long long rows, int size, const char *name, size_t *bytes)
+{
+    if (stride == 0) stride = elems;
+    if (stride < elems)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is smaller than a row");
+    if (stride * size % 16 != 0)
+        return fail(SKETCHSSM_ERR_ALIGNMENT, std::string(name) + " stride is not a multiple of 16 bytes");
+    if (stride > (1LL << 40)) return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is too large");
+    *bytes = rows ? (size_t)((rows - 1) * stride + elems) * size : 0;
+    return SKETCHSSM_OK;
+}
+
+// cu NULL: one token a row
+sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc *td, int32_t rows, int32_t tokens,
+                            bool chunk, const int32_t *cu, const int32_t *slot, const void *q, const void *k,
+                            const void *v, const float *a, const float *beta, float *S, void *y,
+                            sketchssm_stream stream)
+{
+    g_last_error.clear();
+    sketchssm_status s = check_plan(p);
+    if (s != SKETCHSSM_OK) return s;
+    if (!td) return fail(SKETCHSSM_ERR_INVALID_ARG, "token desc is NULL");
+    const sketchssm_desc &d = p->d;
+    if (d.kind != SKETCHSSM_GDN)
+        return fail(SKETCHSSM_ERR_UNSUPPORTED, "the gated delta rule needs a plan of kind SKETCHSSM_GDN");
+    if (td->dtype < SKETCHSSM_F32 || td->dtype > SKETCHSSM_F16)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, "unknown token dtype");
+    if (rows < 0 || tokens < 0) return fail(SKETCHSSM_ERR_INVALID_ARG, "a negative count of rows or tokens");
+    if (!slot && rows > d.batch)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, "more rows than states, and no slots");
+    if (!chunk) tokens = rows;
+    const long long B = d.batch, H = d.heads, Q = d.qk_heads, K = d.key_dim, V = d.value_dim, N = tokens;
+    sk::DeltaArgs A;
+    A.q_stride = td->q_stride;
+    A.k_stride = td->k_stride;
+    A.v_stride = td->v_stride;
+    A.y_stride = td->y_stride;
+    const int es = dtype_size(td->dtype);
+    size_t qb, kb, vb, yb;
+    if ((s = row_span(A.q_stride, Q * K, N, es, "q", &qb)) != SKETCHSSM_OK ||
+        (s = row_span(A.k_stride, Q * K, N, es, "k", &kb)) != SKETCHSSM_OK ||
+        (s = row_span(A.v_stride, H * V, N, es, "v", &vb)) != SKETCHSSM_OK ||
+        (s = row_span(A.y_stride, H * V, N, es, "y", &yb)) != SKETCHSSM_OK)
+        return s;
+    A.VS = sk::step_slab(d.value_dim);
+    if ((long long)rows * H * (V / A.VS) > 0x7fffffffLL)
+        return fail(SKETCHSSM_ERR_UNSUPPORTED, "rows * heads too large for one launch");
+    if (rows == 0 || tokens == 0) return SKETCHSSM_OK;
+    if (chunk) CHECK_I(cu, sizeof(int32_t) * ((size_t)rows + 1), "cu", false);
+    CHECK_I(slot, sizeof(int32_t) * (size_t)rows, "slot", true);
+    CHECK_T(q, qb, "q", false);
+    CHECK_T(k, kb, "k", false);
+    CHECK_T(v, vb, "v", false);
+    CHECK_I(a, fbytes(N, H), "a", false);
+    CHECK_I(beta, fbytes(N, H), "beta", false);
+    CHECK_T(S, fbytes(B, H, K, V), "S", false);
+    CHECK_T(y, yb, "y", false);
+    A.dtype = td->dtype;
+    A.rows = rows;
+    A.tokens = tokens;
+    A.slots = d.batch;
+    A.H = d.heads;
+    A.Hqk = d.qk_heads;
+    A.V = d.value_dim;
+    A.hpq = p->hpq;
+    A.normalize = td->normalize_qk != 0;
+    A.scale = td->scale;
+    A.cu = chunk ? cu : nullptr;
+    A.slot = slot;
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.a = a;
+    A.beta = beta;
+    A.S = S;
+    A.y = y;
+    A.status = p->d_status;
+    A.wait_limit = p->wait_limit;
+    cudaError_t e = sk::launch_delta(A, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "delta rule kernel launch");
+    return SKETCHSSM_OK;
+}
+
+}  // namespace
+
+extern "C" sketchssm_status sketchssm_delta_chunk(const sketchssm_plan *p, const sketchssm_token_desc *td,
+                                                  int32_t seqs, int32_t tokens, const int32_t *cu,
+                                                  const int32_t *slot, const void *q, const void *k, const void *v,
+                                                  const float *a, const float *beta, float *S, void *y,
+                                                  sketchssm_stream stream)
+{
+    return delta_impl(p, td, seqs, tokens, true, cu, slot, q, k, v, a, beta, S, y, stream);
+}
+
+extern "C" sketchssm_status sketchssm_delta_step(const sketchssm_plan *p, const sketchssm_token_desc *td,
+                                                 int32_t rows, const int32_t *slot, const void *q, const void *k,
+                                                 const void *v, const float *a, const float *beta, float *S, void *y,
+                                                 sketchssm_stream stream)
+{
+    return delta_impl(p, td, rows, 0, false, nullptr, slot, q, k, v, a, beta, S, y, stream);
+}
+
+extern "C" sketchssm_status sketchssm_gated_norm(const sketchssm_norm_desc *nd, int32_t rows, const void *x,
+                                                 const void *z, const float *weight, void *out,
+                                                 sketchssm_stream stream)
+{
+    g_last_error.clear();
+    if (!nd) return fail(SKETCHSSM_ERR_INVALID_ARG, "norm desc is NULL");
+    if (nd->x_dtype < SKETCHSSM_F32 || nd->x_dtype > SKETCHSSM_F16 || nd->dtype < SKETCHSSM_F32 ||
+        nd->dtype > SKETCHSSM_F16)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, "unknown dtype");
+    if (nd->gate < SKETCHSSM_SILU || nd->gate > SKETCHSSM_SIGMOID) return fail(SKETCHSSM_ERR_INVALID_ARG, "unknown gate");
+    if (rows < 0 || nd->groups < 1 || nd->width < 1)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, "rows >= 0, groups >= 1 and width >= 1 are needed");
+    if (nd->weight_groups != 1 && nd->weight_groups != nd->groups)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, "weight_groups must be 1 or groups");
+    if (!(nd->eps >= 0.f)) return fail(SKETCHSSM_ERR_INVALID_ARG, "eps must not be negative");
+    if (nd->width % 8 != 0 || nd->width > sk::NORM_MAX_WIDTH)
+        return fail(SKETCHSSM_ERR_UNSUPPORTED, "width must be a multiple of 8 up to 16384");
+    sk::NormArgs A;
+    A.x_stride = nd->x_stride;
+    A.z_stride = nd->z_stride;
+    A.out_stride = nd->out_stride;
+    const long long elems = (long long)nd->groups * nd->width;
+    size_t xb, zb, ob;
+    sketchssm_status s;
+    if ((s = row_span(A.x_stride, elems, rows, dtype_size(nd->x_dtype), "x", &xb)) != SKETCHSSM_OK ||
+        (s = row_span(A.z_stride, elems, rows, dtype_size(nd->dtype), "z", &zb)) != SKETCHSSM_OK ||
+        (s = row_span(A.out_stride, elems, rows, dtype_size(nd->dtype), "out", &ob)) != SKETCHSSM_OK)
+        return s;
+    A.items = (long long)rows * nd->groups;
+    if (A.items > 0x7fffffffLL) return fail(SKETCHSSM_ERR_UNSUPPORTED, "rows * groups too large for one launch");
+    if (rows == 0) return SKETCHSSM_OK;
+    CHECK_T(x, xb, "x", false);
+    CHECK_T(z, zb, "z", true);
+    CHECK_T(weight, fbytes(nd->weight_groups, nd->width), "weight", false);
+    CHECK_T(out, ob, "out", false);
+    A.x_dtype = nd->x_dtype;
+    A.dtype = nd->dtype;
+    A.groups = nd->groups;
+    A.width = nd->width;
+    A.weight_groups = nd->weight_groups;
+    A.sigmoid = nd->gate == SKETCHSSM_SIGMOID;
+    A.gate_first = nd->gate_first != 0;
+    A.eps = nd->eps;
+    A.x = x;
+    A.z = z;
+    A.weight = weight;
+    A.out = out;
+    cudaError_t e = sk::launch_gated_norm(A, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "gated norm kernel launch");
     return SKETCHSSM_OK;
 }
