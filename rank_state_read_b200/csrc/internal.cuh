@@ -21,6 +21,7 @@ constexpr int SK_STATUS_FLUSH_TIMEOUT = 2;
 constexpr int SK_STATUS_STEP_TIMEOUT = 4;
 constexpr int SK_STATUS_BAD_ROW = 8;  // a per-row position or token count out of range
 constexpr int SK_STATUS_PREFILL_TIMEOUT = 16;
+constexpr int SK_STATUS_DELTA_TIMEOUT = 32;
 
 // default bound of a kernel's wait on its own bulk copies (clock cycles, ~1 s)
 constexpr long long DEFAULT_WAIT_CYCLES = 2000000000LL;
@@ -133,6 +134,10 @@ struct DeltaArgs {
     long long wait_limit;
 };
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t stream);
+// prompts of 16-bit tokens, 64 at a time on the tensor cores
+constexpr int DC_MAX_SEQS = 2048;
+bool delta_chunk_fits(const DeltaArgs &a);
+cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream);
 
 // The gated norm: `items` = rows x groups, each of `width` values.
 constexpr int NORM_MAX_WIDTH = 16384;

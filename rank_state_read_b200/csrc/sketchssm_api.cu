@@ -390,13 +390,15 @@ sketchssm_status sketchssm_plan_check(const sketchssm_plan *p, sketchssm_stream 
         return fail(SKETCHSSM_ERR_TIMEOUT, "a decode CTA waited past the plan's limit for its bulk copies");
     if (flags & sk::SK_STATUS_BAD_ROW)
         return fail(SKETCHSSM_ERR_INVALID_ARG,
-                    "a per-row position or token count was out of range; those rows were left unchanged");
+                    "a per-row position, token count, slot or range was out of range (or a slot named twice); those rows were left unchanged");
     if (flags & sk::SK_STATUS_STEP_TIMEOUT)
         return fail(SKETCHSSM_ERR_TIMEOUT, "a standard-step CTA waited past the plan's limit for its bulk copies");
     if (flags & sk::SK_STATUS_FLUSH_TIMEOUT)
         return fail(SKETCHSSM_ERR_TIMEOUT, "a flush CTA waited past the plan's limit for its bulk copies");
     if (flags & sk::SK_STATUS_PREFILL_TIMEOUT)
         return fail(SKETCHSSM_ERR_TIMEOUT, "a prefill CTA waited past the plan's limit for its tensor-core products");
+    if (flags & sk::SK_STATUS_DELTA_TIMEOUT)
+        return fail(SKETCHSSM_ERR_TIMEOUT, "a delta-rule CTA waited past the plan's limit for its tensor-core products");
     return SKETCHSSM_OK;
 }
 
@@ -821,7 +823,8 @@ sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc 
     A.y = y;
     A.status = p->d_status;
     A.wait_limit = p->wait_limit;
-    cudaError_t e = sk::launch_delta(A, (cudaStream_t)stream);
+    cudaError_t e = sk::delta_chunk_fits(A) ? sk::launch_delta_chunk(A, p->sms, (cudaStream_t)stream)
+                                            : sk::launch_delta(A, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule kernel launch");
     return SKETCHSSM_OK;
 }
