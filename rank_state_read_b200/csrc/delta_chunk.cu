@@ -43,9 +43,10 @@ constexpr int DC_C = 64;        // tokens of a chunk
 constexpr int DC_VW = 128;      // value columns of a slice
 constexpr int DC_CHAIN = 256, DC_PREP = 128;
 constexpr int DC_THREADS = DC_CHAIN + DC_PREP + 128;
-// registers a thread after the split: 2 x 128 x 160 + 128 x 152 + 128 x 40 = 512 x 128
-constexpr int DC_REG_CHAIN = 160, DC_REG_PREP = 152, DC_REG_ISSUE = 40;
-constexpr int DC_KV = 3, DC_TP = 2;  // stages of q, k, v and of T, P
+// registers a thread after the split: 2 x 128 x 168 + 128 x 120 + 128 x 56 = 512 x 128
+constexpr int DC_REG_CHAIN = 168, DC_REG_PREP = 120, DC_REG_HELP = 56;
+constexpr int DC_KV = 3;        // stages of q and k; everything else has two
+constexpr float DC_STRONG = 100.f;  // exponents of a chunk's decays within which 2^(G_i - G_j) factors
 
 // tensor memory columns
 constexpr uint32_t TM_A = 0;     // K S^T, then U^T (64); with the next 64: the state's increment
@@ -58,17 +59,19 @@ constexpr uint32_t TM_KK = 448;  // [K; Q] K^T (64)
 struct DcSmem {
     // 1024-byte aligned operand tiles, rows of 128 bytes, 128-byte swizzle
     uint8_t kq[DC_KV][2][128 * 128];  // k dims 0-63 | 64-127; rows 0-63 k, 64-127 q
-    uint8_t tp[DC_TP][4][64 * 128];   // T hi, T lo (before that A and T in fp32), P hi, P lo
-    uint16_t v[DC_KV][DC_C][DC_VW];
-    float ab[DC_KV][128];             // beta, a of the chunk's tokens
-    // per token, by T / P stage: factors of v and K S in R; of U; of U for the state; of Q S; of P U
-    float fv[DC_TP][DC_C], fks[DC_TP][DC_C], fu[DC_TP][DC_C], fw[DC_TP][DC_C], fqs[DC_TP][DC_C], fp[DC_TP][DC_C];
-    alignas(16) float fac[128];       // value of a unit of each k and q row
-    alignas(16) float Gh[DC_C], Gl[DC_C];  // G in base 2, high and low parts
-    float gC[DC_TP];                  // the whole chunk's decay
+    uint8_t tp[2][4][64 * 128];       // T hi, T lo, P hi, P lo
+    float m[64 * 64];                 // A, then T, in fp32
+    uint16_t v[2][DC_C][DC_VW];       // values, then outputs
+    // per token: factors of v and K S in R; of U; of U for the state; of Q S; of P U
+    float fv[2][DC_C], fks[2][DC_C], fu[2][DC_C], fw[2][DC_C], fqs[2][DC_C], fp[2][DC_C];
+    // per token: beta; 2^G; 2^(G_63 - G); 2^(G - G_31) and its inverse; G, high and low part
+    float beta[2][DC_C], dec[2][DC_C], rest[2][DC_C], er[2][DC_C], ec[2][DC_C], gh[2][DC_C], gl[2][DC_C];
+    float col[DC_C];                  // factor of k_j in A and P
     float x[32][36];                  // products on the way to T
     float mx[2][2][2][DC_VW];         // column maxima of the two chain halves
-    uint64_t b_kq[DC_KV], b_free[DC_KV], b_tp[DC_TP], b_out[DC_TP];
+    float gC[2];                      // the whole chunk's decay
+    int strong[2];
+    uint64_t b_ld[DC_KV], b_free[DC_KV], b_kq[DC_KV], b_v[2], b_vfree[2], b_sc[2], b_tp[2], b_out[2];
     uint64_t b_S, b_KS, b_QS, b_R, b_U, b_W, b_D, b_PU, b_KK, b_end;
     uint32_t taddr;
     int stop;
@@ -128,6 +131,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// 16 columns
+__device__ __forceinline__ void tmem_ld16n(uint32_t addr, float *x)
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(x);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -160,83 +174,107 @@ __device__ __forceinline__ void pow2_scale(float m, float &mul, float &inv)
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
 // hi and lo fp16 parts of two scaled values
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
 {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
+    const __half2 h = __float22half2_rn(v);
     hi = h2_bits(h);
-    lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+    lo = h2_bits(__float22half2_rn(__ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), v)));
+}
+
+__device__ __forceinline__ float max3(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
+
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
+// two neighbouring values of a per-token array in shared memory, four at a time
+struct Four {
+    float2 a, b;
+};
+__device__ __forceinline__ Four lds_four(const float *p)
+{
+    const float4 v = lds4(p);
+    return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // ---- which chunk comes next ----
 
 static_assert(sizeof(DcSmem) <= 232448, "shared memory of one CTA");
 static_assert(offsetof(DcSmem, kq) % 1024 == 0 && offsetof(DcSmem, tp) % 1024 == 0, "swizzled tiles");
-static_assert(offsetof(DcSmem, v) % 16 == 0 && offsetof(DcSmem, fac) % 16 == 0 && offsetof(DcSmem, Gh) % 16 == 0 &&
-                  offsetof(DcSmem, Gl) % 16 == 0 && offsetof(DcSmem, b_kq) % 8 == 0,
+static_assert(offsetof(DcSmem, m) % 16 == 0 && offsetof(DcSmem, v) % 16 == 0 && offsetof(DcSmem, fv) % 16 == 0 &&
+                  offsetof(DcSmem, beta) % 16 == 0 && offsetof(DcSmem, col) % 16 == 0 && offsetof(DcSmem, b_ld) % 8 == 0,
               "vector accesses");
 
 struct DcWalk {
-    int round, chunk;   // of this CTA's items; chunk of the item
-    int h, slice, len;
-    long long first, slot;
+    int item;           // in this CTA's order
+    int chunk;          // of the item
+    int h, slice, len, first, slot;
     bool there;
 };
 
 __device__ __forceinline__ void dc_fetch(const DeltaArgs &A, const DcSmem &sm, DcWalk &w)
 {
-    const int nslice = (A.V + DC_VW - 1) / DC_VW, per = A.H * nslice;
-    const int items = A.rows * per, G = gridDim.x;
+    const unsigned nslice = (unsigned)(A.V + DC_VW - 1) / DC_VW, per = A.H * nslice;
+    const unsigned items = A.rows * per, G = gridDim.x;
     w.chunk = 0;
-    for (;; ++w.round) {
+    w.there = false;
+#pragma unroll 1
+    for (;; ++w.item) {
         // items go round back and forth, so that a CTA that gets a longer one gets a shorter
         // one next
-        const long long k = (long long)w.round * G + ((w.round & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if ((long long)w.round * G >= items) {
-            w.there = false;
-            return;
-        }
+        const unsigned base = w.item * G;
+        if (base >= items) return;
+        const unsigned k = base + ((w.item & 1) ? G - 1 - blockIdx.x : blockIdx.x);
         if (k >= items) continue;
         const int row = sm.order[k / per], rest = (int)(k % per);
-        const int c0 = __ldg(A.cu + row), c1 = __ldg(A.cu + row + 1), slot = A.slot ? __ldg(A.slot + row) : row;
-        if (c0 < 0 || c1 <= c0 || c1 > A.tokens || slot < 0 || slot >= A.slots || (sm.dup[row >> 5] >> (row & 31) & 1))
+        w.first = __ldg(A.cu + row);
+        const int end = __ldg(A.cu + row + 1);
+        w.slot = A.slot ? __ldg(A.slot + row) : row;
+        if (w.first < 0 || end <= w.first || end > A.tokens || w.slot < 0 || w.slot >= A.slots ||
+            (sm.dup[row >> 5] >> (row & 31) & 1))
             continue;
-        w.there = true;
-        w.first = c0;
-        w.len = c1 - c0;
-        w.slot = slot;
+        w.len = end - w.first;
         w.h = rest / nslice;
-        w.slice = rest % nslice;
+        w.slice = rest - w.h * nslice;
+        w.there = true;
         return;
     }
 }
 
+__device__ __forceinline__ void dc_start(DcWalk &w)
+{
+    w.item = -1;
+    w.chunk = w.len = 0;
+    w.there = true;
+}
+
+// the next chunk of this CTA (the first one after dc_start)
 __device__ __forceinline__ void dc_next(const DeltaArgs &A, const DcSmem &sm, DcWalk &w)
 {
-    if (!w.there) return;
-    if (++w.chunk * DC_C < w.len) return;
-    ++w.round;
+    if (!w.there || ++w.chunk * DC_C < w.len) return;
+    ++w.item;
     dc_fetch(A, sm, w);
 }
 
 // ---- waits: bounded; past the plan's limit recorded, past the default limit given up, after
 // which nothing waits any more and the kernel runs out ----
-__device__ __forceinline__ void dc_wait_long(const DeltaArgs &A, DcSmem &sm, uint64_t *bar, uint32_t parity)
-{
-    if (*(volatile int *)&sm.stop) return;
-    atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity))
-        if (clock64() - t0 > DEFAULT_WAIT_CYCLES || *(volatile int *)&sm.stop) {
-            *(volatile int *)&sm.stop = 1;
-            return;
-        }
-}
-
 __device__ __forceinline__ void dc_wait(const DeltaArgs &A, DcSmem &sm, uint64_t *bar, uint32_t parity)
 {
     if (mbar_test_wait(bar, parity)) return;
-    if (!mbar_wait_bounded(bar, parity, A.wait_limit)) dc_wait_long(A, sm, bar, parity);
+    const long long t0 = clock64();
+    do {
+        const long long t = clock64() - t0;
+        if (t > A.wait_limit) {
+            atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
+            if (t > DEFAULT_WAIT_CYCLES) *(volatile int *)&sm.stop = 1;
+            if (*(volatile int *)&sm.stop) return;
+        }
+    } while (!mbar_try_wait(bar, parity));
 }
 
 // one arrival for a warp whose lanes have all done their part
@@ -246,48 +284,160 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// ---- warps 8-11 ----
+// ---- warp 15: q, k, v of one chunk after the other, a row of 256 (128) bytes a copy; a row of
+// k or q lands unswizzled (the conversion reads it so) ----
 
-// cp.async of 16 bytes, or 16 zero bytes
-__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
-                 : "memory");
-}
-
-// k, q, v, beta and a of the walk's chunk into stage `st`; rows past the sequence's end are zeros
 template <class T>
-__device__ __forceinline__ void dc_load(const DeltaArgs &A, DcSmem &sm, const DcWalk &w, int st, int r)
+__device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm)
 {
-    const long long t0 = w.first + (long long)w.chunk * DC_C;
-    const int left = w.len - w.chunk * DC_C;
-    const int hq = w.h / A.hpq;
-    const int vw = min(DC_VW, A.V - w.slice * DC_VW);
-    // 16 threads a row of k or q, 8 rows a pass
-    const int c = r & 15, r0 = r >> 4;
-    const T *kp = static_cast<const T *>(A.k) + hq * KDIM + c * 8, *qp = static_cast<const T *>(A.q) + hq * KDIM + c * 8;
-    uint8_t *dst = sm.kq[st][c >> 3];
+    const int lane = threadIdx.x & 31;
+    DcWalk w;
+    dc_start(w);
+    for (int n = 0;; ++n) {
+        dc_next(A, sm, w);
+        if (!w.there) break;
+        const int st = n % DC_KV, sv = n & 1;
+        const long long t0 = w.first + w.chunk * DC_C;
+        const int rows = min(w.len - w.chunk * DC_C, DC_C);
+        const int hq = w.h / A.hpq;
+        const uint32_t vb = (uint32_t)min(DC_VW, A.V - w.slice * DC_VW) * 2;
+        if (n >= DC_KV) dc_wait(A, sm, &sm.b_free[st], (n / DC_KV - 1) & 1);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.b_ld[st], (uint32_t)rows * 512);
+        __syncwarp();
+        for (int t = lane; t < rows; t += 32) {
+            const T *k = static_cast<const T *>(A.k) + (t0 + t) * A.k_stride + hq * KDIM;
+            const T *q = static_cast<const T *>(A.q) + (t0 + t) * A.q_stride + hq * KDIM;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = i * 8 + r0;  // t & 7 == r0
-        const bool there = t < left;
-        const long long tok = t0 + (there ? t : 0);
-        const int off = t * 128 + (((c & 7) ^ r0) << 4);
-        cp_async16_zfill(dst + off, kp + tok * A.k_stride, there);
-        cp_async16_zfill(dst + 64 * 128 + off, qp + tok * A.q_stride, there);
-    }
-    if (c * 8 < vw) {
-        const T *vp = static_cast<const T *>(A.v) + (long long)w.h * A.V + w.slice * DC_VW + c * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = i * 8 + r0;
-            const bool there = t < left;
-            cp_async16_zfill(&sm.v[st][t][c * 8], vp + (t0 + (there ? t : 0)) * A.v_stride, there);
+            for (int i = 0; i < 2; ++i) {
+                bulk_copy_g2s(sm.kq[st][i] + t * 128, k + 64 * i, 128, &sm.b_ld[st]);
+                bulk_copy_g2s(sm.kq[st][i] + (64 + t) * 128, q + 64 * i, 128, &sm.b_ld[st]);
+            }
         }
+        if (n >= 2) dc_wait(A, sm, &sm.b_vfree[sv], (n / 2 - 1) & 1);
+        // rows past the sequence's end count as zeros
+        for (int i = rows * (DC_VW / 8) + lane; i < DC_C * (DC_VW / 8); i += 32)
+            *reinterpret_cast<uint4 *>(&sm.v[sv][i / (DC_VW / 8)][i % (DC_VW / 8) * 8]) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&sm.b_v[sv], (uint32_t)rows * vb);
+        __syncwarp();
+        for (int t = lane; t < rows; t += 32)
+            bulk_copy_g2s(sm.v[sv][t], static_cast<const T *>(A.v) + (t0 + t) * A.v_stride + (long long)w.h * A.V + w.slice * DC_VW,
+                          vb, &sm.b_v[sv]);
     }
-    const int t = r & 63;
-    if (t < left) cp_async4(&sm.ab[st][r], (r < 64 ? A.beta : A.a) + (t0 + t) * A.H + w.h);
 }
+
+// ---- warp 13: outputs, from the place of their chunk's values ----
+
+template <class T>
+__device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm)
+{
+    const int lane = threadIdx.x & 31;
+    DcWalk w;
+    dc_start(w);
+    for (int n = 0;; ++n) {
+        dc_next(A, sm, w);
+        if (!w.there) break;
+        const int sv = n & 1;
+        const long long t0 = w.first + w.chunk * DC_C;
+        const int rows = min(w.len - w.chunk * DC_C, DC_C);
+        const uint32_t vb = (uint32_t)min(DC_VW, A.V - w.slice * DC_VW) * 2;
+        dc_wait(A, sm, &sm.b_out[sv], (n / 2) & 1);
+        for (int t = lane; t < rows; t += 32) {
+            T *y = static_cast<T *>(A.y) + (t0 + t) * A.y_stride + (long long)w.h * A.V + w.slice * DC_VW;
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(y), "r"(smem_addr(sm.v[sv][t])),
+                         "r"(vb)
+                         : "memory");
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        warp_arrive(&sm.b_vfree[sv]);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// ---- warp 14: the decays of a chunk's tokens, two tokens a lane ----
+
+__device__ __forceinline__ float pow2_of(long long d)  // 2^(d / 2^40), to fp32 accuracy
+{
+    const int i = (int)(d >> 40);
+    const float f = (float)(int)((d >> 16) & 0xffffff) * 0x1p-24f;
+    // exponents below the normal range give 0, above it infinity
+    return i < -126 ? 0.f : i > 127 ? __int_as_float(0x7f800000) : ex2(f) * __int_as_float((i + 127) << 23);
+}
+
+__device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
+{
+    const int lane = threadIdx.x & 31;
+    DcWalk w;
+    dc_start(w);
+    float a[2], beta[2];
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const bool there = w.there && w.chunk * DC_C + t < w.len;
+            const long long at = (long long)(w.first + w.chunk * DC_C + t) * A.H + w.h;
+            a[i] = there ? __ldg(A.a + at) : 1.f;
+            beta[i] = there ? __ldg(A.beta + at) : 0.f;
+        }
+    };
+    long long G[2], mid, end, top;
+    float be[2];
+    unsigned bad = 0;
+    for (int n = -1;; ++n) {
+        const int b = n & 1;
+        const bool any = w.there;  // chunk n, whose a and beta are here
+        if (n >= 0) {
+            if (!any) break;
+            // log2 a in steps of 2^-40: sums and differences are exact.  A decay of 0 counts as
+            // 2^-150, which no fp32 product tells from it; a decay that is no number stays one.
+            long long l[2];
+            bool nan[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = log2f(a[i]);
+                nan[i] = !(x == x);
+                l[i] = (long long)(fminf(fmaxf(x, -150.f), 150.f) * 0x1p40f);
+            }
+            be[0] = beta[0], be[1] = beta[1];
+            bad = __ballot_sync(0xffffffffu, nan[0] || nan[1]);
+            long long s = l[0] + l[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += up;
+            }
+            G[0] = s - l[1], G[1] = s;
+            mid = __shfl_sync(0xffffffffu, G[1], 15);
+            end = __shfl_sync(0xffffffffu, G[1], 31);
+            top = __shfl_sync(0xffffffffu, G[0], 0);
+        }
+        dc_next(A, sm, w);
+        load();  // those of chunk n + 1, on their way while chunk n's are written down
+        if (n < 0) continue;
+        if (n >= 2) dc_wait(A, sm, &sm.b_tp[b], (n / 2 - 1) & 1);  // chunk n - 2 has been prepared
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const bool lost = bad & (0xffffffffu >> (31 - lane));  // from that token on
+            const float g = (float)G[i] * 0x1p-40f;
+            sm.beta[b][t] = be[i];
+            sm.dec[b][t] = lost ? __int_as_float(0x7fc00000) : pow2_of(G[i]);
+            sm.rest[b][t] = pow2_of(end - G[i]);
+            sm.er[b][t] = pow2_of(G[i] - mid);
+            sm.ec[b][t] = pow2_of(mid - G[i]);
+            sm.gh[b][t] = g;
+            sm.gl[b][t] = (float)(G[i] - (long long)(g * 0x1p40f)) * 0x1p-40f;
+        }
+        if (lane == 0) {
+            const float span = fmaxf((float)(top - mid), (float)(mid - end)) * 0x1p-40f;
+            sm.strong[b] = !(span < DC_STRONG) || (float)(end - top) * 0x1p-40f > DC_STRONG;
+        }
+        warp_arrive(&sm.b_sc[b]);
+    }
+}
+
+// ---- warps 8-11 ----
 
 // where A and T lie in fp32: rows of 64 floats, 16-byte chunks permuted by the row
 __device__ __forceinline__ int tri(int i, int j) { return i * 64 + ((((j >> 2) ^ i) & 15) << 2) + (j & 3); }
@@ -307,12 +457,14 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], con
                    "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b[0])), "r"(__float_as_uint(b[1])));
 }
 
-// D (MT tiles of 16 rows x 8 columns) += L[16 MT x 8 KT] B[8 KT x 8], three tf32 products each:
-// fp32 accuracy.  l(i, k), b(k, n): the operands' elements.
+// L[16 MT x 8 KT] B[8 KT x 8] as MT tiles of 16 rows x 8 columns, three tf32 products each (in
+// accumulators of their own, so that none waits for another): fp32 accuracy.  l(i, k), b(k, n):
+// the operands' elements.
 template <int MT, int KT, class FL, class FB>
 __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float d1[MT][4] = {}, d2[MT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < KT; ++ks) {
         float bh[2], bl[2];
@@ -331,11 +483,15 @@ __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
                 ah[e] = tf32_round(x);
                 al[e] = x - ah[e];
             }
-            mma_tf32(d[m], al, bh);
-            mma_tf32(d[m], ah, bl);
+            mma_tf32(d1[m], al, bh);
+            mma_tf32(d2[m], ah, bl);
             mma_tf32(d[m], ah, bh);
         }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[m][e] += d1[m][e] + d2[m][e];
 }
 
 // T = (I + A)^-1 in place, A strictly lower triangular (zeros elsewhere), by the four warps of
@@ -405,94 +561,85 @@ __device__ __forceinline__ void invert(float *M, float (&X)[32][36], int r)
     named_sync(5, DC_PREP);
 }
 
-// 64 scaled values as fp16 hi (and lo) parts into row `t` of a swizzled tile
-template <bool LO>
-__device__ __forceinline__ void put_row(uint8_t *hi, uint8_t *lo, int t, const float (&x)[64], float mul)
+// 16 scaled values as fp16 parts into columns 16 c .. of row `t` of two swizzled tiles
+__device__ __forceinline__ void put16(uint8_t *hi, uint8_t *lo, int t, int c, const float2 (&x)[8], float mul)
 {
+    uint32_t h[8], l[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t h[4], l[4];
+    for (int e = 0; e < 8; ++e) split2(__fmul2_rn(x[e], two(mul)), h[e], l[e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2(x[8 * c + 2 * e] * mul, x[8 * c + 2 * e + 1] * mul, h[e], l[e]);
-        const int off = t * 128 + ((c ^ (t & 7)) << 4);
-        *reinterpret_cast<uint4 *>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (LO) *reinterpret_cast<uint4 *>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int i = 0; i < 2; ++i) {
+        const int off = t * 128 + (((2 * c + i) ^ (t & 7)) << 4);
+        *reinterpret_cast<uint4 *>(hi + off) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        *reinterpret_cast<uint4 *>(lo + off) = make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
     }
 }
 
-template <class T, bool LO>
+template <class T>
 __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
-    const int r = threadIdx.x - DC_CHAIN, wq = r >> 5, lane = r & 31;
+    const int r = threadIdx.x - DC_CHAIN, wq = r >> 5;
     const int t = r & 63;        // token of this thread's row
     const bool is_q = r >= 64;
-    DcWalk w, ahead;
-    w.round = 0;
-    dc_fetch(A, sm, w);
-    ahead = w;
-    for (int i = 0; i < 2; ++i) {
-        if (ahead.there) dc_load<T>(A, sm, ahead, i, r);
-        cp_async_commit();
-        dc_next(A, sm, ahead);
-    }
-    for (int n = 0; w.there; ++n, dc_next(A, sm, w)) {
-        const int st = n % DC_KV, tp = n % DC_TP;
+    const uint32_t kk = tmem + TM_KK + ((uint32_t)(wq * 32) << 16);
+    DcWalk w;
+    dc_start(w);
+    for (int n = 0;; ++n) {
+        dc_next(A, sm, w);
+        if (!w.there) break;
+        const int st = n % DC_KV, tp = n & 1;
         const int left = w.len - w.chunk * DC_C;
-        cp_async_wait<1>();
-        named_sync(5, DC_PREP);
+        dc_wait(A, sm, &sm.b_ld[st], (n / DC_KV) & 1);
 
-        // this thread's row of k or q: its norm, and fp16 values at a power of two of their own
+        // this thread's row of k or q: its norm, and fp16 values at a power of two of their own,
+        // from plain to swizzled order (a half row at a time: position c takes what c ^ (r & 7) held)
+        float f_own;
         {
-            uint4 raw[16];
+            uint8_t *row[2] = {sm.kq[st][0] + r * 128, sm.kq[st][1] + r * 128};
+            const int sw = (r & 7) << 4;
+            const bool there = t < left;
+            float2 s2 = two(0.f);
+            float m = 0.f;
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                raw[c] = *reinterpret_cast<const uint4 *>(&sm.kq[st][c >> 3][r * 128 + (((c & 7) ^ (r & 7)) << 4)]);
-            float ss = 0.f, m = 0.f;
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll 4
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 raw = *reinterpret_cast<const uint4 *>(row[hf] + ((c << 4) ^ sw));
+                    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack2(v[e], (const T *)nullptr);
-                    ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
-                    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2(v[e], (const T *)nullptr);
+                        s2 = __ffma2_rn(f, f, s2);
+                        m = max3(m, f);
+                    }
                 }
-            }
             float mul, inv;
             pow2_scale(m, mul, inv);
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                uint4 o[8];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-                uint32_t o[4];
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 raw = *reinterpret_cast<const uint4 *>(row[hf] + ((c << 4) ^ sw));
+                    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+                    uint32_t p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack2(v[e], (const T *)nullptr);
-                    o[e] = h2_bits(__floats2half2_rn(f.x * mul, f.y * mul));
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
+                        if (!there) p[e] = 0;
+                    }
+                    o[c] = make_uint4(p[0], p[1], p[2], p[3]);
                 }
-                *reinterpret_cast<uint4 *>(&sm.kq[st][c >> 3][r * 128 + (((c & 7) ^ (r & 7)) << 4)]) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            if (A.normalize) inv *= rsqrtf(ss + DELTA_QK_EPS);
-            if (is_q) inv *= A.scale;
-            sm.fac[r] = inv;
-        }
-        if (wq == 0) {
-            // G of tokens 2 l and 2 l + 1, base 2, summed in 64 bits
-            const float a0 = 2 * lane < left ? sm.ab[st][64 + 2 * lane] : 1.f;
-            const float a1 = 2 * lane + 1 < left ? sm.ab[st][65 + 2 * lane] : 1.f;
-            const double l0 = (double)fmaxf(log2f(a0), -150.f), l1 = (double)fmaxf(log2f(a1), -150.f);
-            double s = l0 + l1;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double up = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += up;
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row[hf] + (c << 4)) = o[c];
             }
-            const double g0 = s - l1;
-            sm.Gh[2 * lane] = (float)g0;
-            sm.Gl[2 * lane] = (float)(g0 - (double)(float)g0);
-            sm.Gh[2 * lane + 1] = (float)s;
-            sm.Gl[2 * lane + 1] = (float)(s - (double)(float)s);
+            if (A.normalize) inv *= rsqrtf(s2.x + s2.y + DELTA_QK_EPS);
+            if (is_q) inv *= A.scale;
+            f_own = there ? inv : 0.f;
         }
+        dc_wait(A, sm, &sm.b_sc[tp], (n / 2) & 1);
+        const bool strong = sm.strong[tp];
+        if (!is_q) sm.col[t] = strong ? f_own : f_own * sm.ec[tp][t];
         fence_async_smem();
         tc_fence_before();
         named_sync(5, DC_PREP);
@@ -500,156 +647,163 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         if (r == 0) {
             tc_fence_after();
             const uint32_t idesc = idesc_f16(128, 64, false);
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 8; ++ks) {
                 const uint64_t d = sdesc_sw128(smem_addr(sm.kq[st][ks >> 2]) + (ks & 3) * 32, 16, 1024);
                 mma_ss(tmem + TM_KK, d, d, idesc, ks > 0);
             }
             umma_commit(&sm.b_KK);
         }
-        // this stage's T, P and factors are free once the chunk two before has given its outputs
-        if (n >= DC_TP) dc_wait(A, sm, &sm.b_out[tp], (n / DC_TP - 1) & 1);
-        const float Gh = sm.Gh[t], Gl = sm.Gl[t];
-        const float beta = t < left ? sm.ab[st][t] : 0.f, f_own = sm.fac[r];
-        const float decay = exp2f(Gh + Gl);
-        float *M = reinterpret_cast<float *>(sm.tp[tp][0]);
+        __syncwarp();
+        const float beta = sm.beta[tp][t], dec = sm.dec[tp][t];
+        float f = is_q ? f_own : f_own * beta;
+        if (!strong) f *= sm.er[tp][t];
+        const int last = is_q ? t : t - 1;
+        const float gh = sm.gh[tp][t], gl = sm.gl[tp][t];
+        // columns 16 c .. of this row of A or P
+        auto entries = [&](int c, float2 (&x)[8]) {
+            tmem_ld16n(kk + 16 * c, reinterpret_cast<float *>(x));
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Four cf = lds_four(sm.col + 16 * c + 4 * e);
+                x[2 * e] = __fmul2_rn(__fmul2_rn(x[2 * e], cf.a), two(f));
+                x[2 * e + 1] = __fmul2_rn(__fmul2_rn(x[2 * e + 1], cf.b), two(f));
+            }
+            if (strong) {
+                // the chunk forgets so much that the factors of its decays leave fp32's range
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 16 * c + 2 * e;
+                    x[e].x *= ex2((gh - sm.gh[tp][j]) + (gl - sm.gl[tp][j]));
+                    x[e].y *= ex2((gh - sm.gh[tp][j + 1]) + (gl - sm.gl[tp][j + 1]));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (16 * c + 2 * e > last) x[e].x = 0.f;
+                if (16 * c + 2 * e + 1 > last) x[e].y = 0.f;
+            }
+        };
         dc_wait(A, sm, &sm.b_KK, n & 1);
         tc_fence_after();
-        {
-            float x[64];
-            tmem_ld32(tmem + TM_KK + ((uint32_t)(wq * 32) << 16), x);
-            tmem_ld32(tmem + TM_KK + 32 + ((uint32_t)(wq * 32) << 16), x + 32);
-            tmem_ld_wait();
-            const float f = is_q ? f_own : f_own * beta;
-            const int last = is_q ? t : t - 1;
-            float m = 0.f;
+        if (!is_q) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float2 x[8];
+                entries(c, x);
 #pragma unroll
-            for (int j4 = 0; j4 < 64; j4 += 4) {
-                const float4 gh = lds4(sm.Gh + j4), gl = lds4(sm.Gl + j4), fj = lds4(sm.fac + j4);
-                const float h[4] = {gh.x, gh.y, gh.z, gh.w}, l[4] = {gl.x, gl.y, gl.z, gl.w}, fk[4] = {fj.x, fj.y, fj.z, fj.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j4 + e;
-                    const float d = exp2f((Gh - h[e]) + (Gl - l[e]));
-                    // factor by factor: k and q rows may be large where their product is not
-                    x[j] = j <= last ? x[j] * fk[e] * f * d : 0.f;
-                    m = fmaxf(m, fabsf(x[j]));
-                }
-            }
-            if (is_q) {
-                float mul, inv;
-                pow2_scale(m, mul, inv);
-                put_row<LO>(sm.tp[tp][2], sm.tp[tp][3], t, x, mul);
-                sm.fp[tp][t] = inv;
-                sm.fqs[tp][t] = decay * f_own;
-            } else {
-#pragma unroll
-                for (int j4 = 0; j4 < 64; j4 += 4) st4(M + tri(t, j4), make_float4(x[j4], x[j4 + 1], x[j4 + 2], x[j4 + 3]));
-                sm.fv[tp][t] = beta;
-                sm.fks[tp][t] = beta * decay * f_own;
-                sm.fw[tp][t] = exp2f((sm.Gh[63] - Gh) + (sm.Gl[63] - Gl)) * f_own;
-                if (t == 63) sm.gC[tp] = decay;
+                for (int e = 0; e < 4; ++e)
+                    st4(sm.m + tri(t, 16 * c + 4 * e), make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y));
             }
         }
+        // this stage of T, P and their factors is free once the chunk two before has given its outputs
+        if (n >= 2) dc_wait(A, sm, &sm.b_out[tp], (n / 2 - 1) & 1);
+        if (is_q) {
+            float m = 0.f, mul, inv;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float2 x[8];
+                entries(c, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = max3(m, x[e]);
+            }
+            pow2_scale(m, mul, inv);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float2 x[8];
+                entries(c, x);
+                put16(sm.tp[tp][2], sm.tp[tp][3], t, c, x, mul);
+            }
+            sm.fp[tp][t] = inv;
+            sm.fqs[tp][t] = dec * f_own;
+        } else {
+            sm.fv[tp][t] = beta;
+            sm.fks[tp][t] = beta * dec * f_own;
+            sm.fw[tp][t] = sm.rest[tp][t] * f_own;
+            if (t == 63) sm.gC[tp] = dec;
+        }
         named_sync(5, DC_PREP);
-        invert(M, sm.x, r);
-        {
-            float x[64];
-            float m = 0.f;
-            if (!is_q) {
+        invert(sm.m, sm.x, r);
+        if (!is_q) {
+            float m = 0.f, mul, inv;
+#pragma unroll 4
+            for (int j4 = 0; j4 < 64; j4 += 4) {
+                const Four v = lds_four(sm.m + tri(t, j4));
+                m = max3(max3(m, v.a), v.b);
+            }
+            pow2_scale(m, mul, inv);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float2 x[8];
 #pragma unroll
-                for (int j4 = 0; j4 < 64; j4 += 4) {
-                    const float4 v = lds4(M + tri(t, j4));
-                    x[j4] = v.x, x[j4 + 1] = v.y, x[j4 + 2] = v.z, x[j4 + 3] = v.w;
+                for (int e = 0; e < 4; ++e) {
+                    const Four v = lds_four(sm.m + tri(t, 16 * c + 4 * e));
+                    x[2 * e] = v.a;
+                    x[2 * e + 1] = v.b;
                 }
-#pragma unroll
-                for (int j = 0; j < 64; ++j) m = fmaxf(m, fabsf(x[j]));
+                put16(sm.tp[tp][0], sm.tp[tp][1], t, c, x, mul);
             }
-            named_sync(5, DC_PREP);  // the fp32 form has been read: its place takes the parts
-            if (!is_q) {
-                float mul, inv;
-                pow2_scale(m, mul, inv);
-                put_row<true>(sm.tp[tp][0], sm.tp[tp][1], t, x, mul);
-                sm.fu[tp][t] = inv;
-            }
+            sm.fu[tp][t] = inv;
         }
         fence_async_smem();
         tc_fence_before();
         warp_arrive(&sm.b_tp[tp]);
-
-        // the chunk after the next, once the chain is through with the chunk before this one
-        if (ahead.there) {
-            if (n >= 1) dc_wait(A, sm, &sm.b_free[(n + 2) % DC_KV], ((n - 1) / DC_KV) & 1);
-            dc_load<T>(A, sm, ahead, (n + 2) % DC_KV, r);
-        }
-        cp_async_commit();
-        dc_next(A, sm, ahead);
+        named_sync(5, DC_PREP);  // T in fp32 has been read
     }
 }
 
 // ---- warp 12 ----
 
-template <bool LO>
 __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
     DcWalk w;
-    w.round = 0;
-    dc_fetch(A, sm, w);
-    const uint32_t i64 = idesc_f16(128, 64, false), i128 = idesc_f16(128, 128, true);
-    for (int n = 0; w.there; ++n, dc_next(A, sm, w)) {
-        const int st = n % DC_KV, tp = n % DC_TP;
-        const uint32_t kq[2] = {smem_addr(sm.kq[st][0]), smem_addr(sm.kq[st][1])};
-        // K S
+    dc_start(w);
+    constexpr uint32_t i64 = idesc_f16(128, 64, false), i128 = idesc_f16(128, 128, true);
+    // descriptors move by bytes / 16: 2 a step of 16 along K, 1024 a half of the key dimensions
+    for (int n = 0;; ++n) {
+        dc_next(A, sm, w);
+        if (!w.there) break;
+        const int st = n % DC_KV, tp = n & 1;
+        const uint64_t k0 = sdesc_sw128(smem_addr(sm.kq[st][0]), 16, 1024);
+        const uint64_t kn = sdesc_sw128(smem_addr(sm.kq[st][0]), 128 * 128, 1024);
+        const uint64_t t0 = sdesc_sw128(smem_addr(sm.tp[tp][0]), 16, 1024);
+        // K S: lo, then hi
         dc_wait(A, sm, &sm.b_kq[st], (n / DC_KV) & 1);
         dc_wait(A, sm, &sm.b_S, n & 1);
         tc_fence_after();
-#pragma unroll
-        for (int p = 1; p >= 0; --p)
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tmem + TM_A, tmem + TM_S + 64 * p + 8 * ks, sdesc_sw128(kq[ks >> 2] + (ks & 3) * 32, 16, 1024), i64,
-                       p == 0 || ks > 0);
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i)
+            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
         umma_commit(&sm.b_KS);
         // Q S, once the chunk before has read its own
-        if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) % DC_TP], ((n - 1) / DC_TP) & 1);
+        if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) & 1], ((n - 1) / 2) & 1);
         tc_fence_after();
-#pragma unroll
-        for (int p = LO ? 1 : 0; p >= 0; --p)
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tmem + TM_Q, tmem + TM_S + 64 * p + 8 * ks,
-                       sdesc_sw128(kq[ks >> 2] + 64 * 128 + (ks & 3) * 32, 16, 1024), i64, (LO && p == 0) || ks > 0);
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i)
+            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
         umma_commit(&sm.b_QS);
-        // U = T R
+        // U = T R: (R lo, T hi), (R hi, T lo), (R hi, T hi)
         dc_wait(A, sm, &sm.b_R, n & 1);
         tc_fence_after();
-        const uint32_t th = smem_addr(sm.tp[tp][0]), tl = smem_addr(sm.tp[tp][1]);
-#pragma unroll
-        for (int p = 0; p < 3; ++p)  // lo hi, hi lo, hi hi
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ts(tmem + TM_A, tmem + TM_R + (p == 0 ? 32 : 0) + 8 * ks, sdesc_sw128((p == 1 ? tl : th) + ks * 32, 16, 1024),
-                       i64, p > 0 || ks > 0);
+#pragma unroll 4
+        for (int i = 0; i < 12; ++i)
+            mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
+                   i > 0);
         umma_commit(&sm.b_U);
         // the state's increment: k as the right operand, tokens along K
         dc_wait(A, sm, &sm.b_W, n & 1);
         tc_fence_after();
-#pragma unroll
-        for (int p = 1; p >= 0; --p)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ts(tmem + TM_A, tmem + TM_S + 32 * p + 8 * ks, sdesc_sw128(kq[0] + ks * 2048, 128 * 128, 1024), i128,
-                       p == 0 || ks > 0);
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
         umma_commit(&sm.b_D);
         umma_commit(&sm.b_free[st]);
-        // P U
-        const uint32_t ph = smem_addr(sm.tp[tp][2]), pl = smem_addr(sm.tp[tp][3]);
-#pragma unroll
-        for (int p = LO ? 0 : 2; p < 3; ++p)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ts(tmem + TM_PU, tmem + TM_S + 64 + (p == 0 ? 32 : 0) + 8 * ks,
-                       sdesc_sw128((p == 1 ? pl : ph) + ks * 32, 16, 1024), i64, (LO && p > 0) || ks > 0);
+        // P U: (U lo, P hi), (U hi, P lo), (U hi, P hi)
+#pragma unroll 4
+        for (int i = 0; i < 12; ++i)
+            mma_ts(tmem + TM_PU, tmem + TM_S + 64 + (i < 4 ? 32 : 0) + 8 * (i & 3),
+                   t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
         umma_commit(&sm.b_PU);
     }
     if (*(volatile int *)&sm.stop) {  // a wait was given up: let what is in flight end before tensor memory goes
@@ -660,7 +814,7 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
 
 // ---- warps 0-7 ----
 
-template <class T, bool LO>
+template <class T>
 __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -677,152 +831,163 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
         b = fmaxf(b, sm.mx[flip][g ^ 1][1][col]);
         flip ^= 1;
     };
-    DcWalk w;
-    w.round = 0;
-    dc_fetch(A, sm, w);
-    float S[64];
-    float sS = 0.f;  // value of a unit of S's parts
-    for (int n = 0; w.there;) {
-        const int vw = min(DC_VW, A.V - w.slice * DC_VW);
-        const bool own = col < vw;
-        const int vcol = w.slice * DC_VW + col;
-        float *Sg = A.S + ((w.slot * A.H + w.h) * KDIM + 64 * g) * A.V + vcol;
-        // parts of S to tensor memory, once nothing reads what lay there
-        auto put_state = [&](bool busy) {
-            float m = 0.f, unused = 0.f, mul;
+    // 32 values (16 pairs) times mul: hi parts to 16 columns at `hi`, lo parts at `lo`
+    auto put = [&](const float2 *x, float mul, uint32_t hi, uint32_t lo) {
+        uint32_t h[16], l[16];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(S[i]));
-            both(m, unused);
-            pow2_scale(m, mul, sS);
-            if (busy) dc_wait(A, sm, &sm.b_PU, (n - 1) & 1);
+        for (int i = 0; i < 16; ++i) split2(__fmul2_rn(x[i], two(mul)), h[i], l[i]);
+        tmem_st16(hi, h);
+        tmem_st16(lo, l);
+    };
+    DcWalk w;
+    dc_start(w);
+    float2 S[32];
+    float *Sg = nullptr;
+    bool own = false, pending = false;
+    float sS = 0.f, sU = 0.f, sW = 0.f, s_old = 0.f;  // values of a unit of the parts of S, U, U~; of S a chunk ago
+    for (int n = 0;; ++n) {
+        const int tp = n & 1, tq = tp ^ 1;  // stages of this chunk and of the one before
+        if (pending) {
+            // the state after the chunk before
+            const float2 gC = two(sm.gC[tq]);
+            dc_wait(A, sm, &sm.b_D, (n - 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                uint32_t hi[16], lo[16];
+                float2 x[16];
+                tmem_ld32(tm + TM_A + 64 * g + 32 * b, reinterpret_cast<float *>(x));
+                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split2(S[32 * b + 2 * i] * mul, S[32 * b + 2 * i + 1] * mul, hi[i], lo[i]);
-                tmem_st16(tm + TM_S + 32 * g + 16 * b, hi);
-                tmem_st16(tm + TM_S + 64 + 32 * g + 16 * b, lo);
+                for (int i = 0; i < 16; ++i)
+                    S[16 * b + i] = __ffma2_rn(two(sW), x[i], __fmul2_rn(gC, S[16 * b + i]));
             }
+            if (w.chunk * DC_C + DC_C >= w.len) {
+                if (own) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        Sg[(long long)(2 * i) * A.V] = S[i].x;
+                        Sg[(long long)(2 * i + 1) * A.V] = S[i].y;
+                    }
+                }
+            }
+        }
+        dc_next(A, sm, w);
+        if (w.there && w.chunk == 0) {
+            own = col < A.V - w.slice * DC_VW;
+            Sg = A.S + (((long long)w.slot * A.H + w.h) * KDIM + 64 * g) * A.V + w.slice * DC_VW + col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                S[i].x = own ? Sg[(long long)(2 * i) * A.V] : 0.f;
+                S[i].y = own ? Sg[(long long)(2 * i + 1) * A.V] : 0.f;
+            }
+        }
+        if (pending) dc_wait(A, sm, &sm.b_PU, (n - 1) & 1);  // nothing reads U's parts any more
+        s_old = sS;
+        if (w.there) {
+            float m = 0.f, unused = 0.f, mul;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = max3(m, S[i]);
+            both(m, unused);
+            pow2_scale(m, mul, sS);
+            tc_fence_after();
+            put(S, mul, tm + TM_S + 32 * g, tm + TM_S + 64 + 32 * g);
+            put(S + 16, mul, tm + TM_S + 32 * g + 16, tm + TM_S + 64 + 32 * g + 16);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&sm.b_S);
-        };
+        }
+        if (pending) {
+            // the outputs of the chunk before, while this one's K S runs: into the place of its values
+            tc_fence_after();
+            float2 q[16], x[16];
+            tmem_ld32(tm + TM_Q + 32 * g, reinterpret_cast<float *>(q));
+            tmem_ld32(tm + TM_PU + 32 * g, reinterpret_cast<float *>(x));
+            tmem_ld_wait();
+            uint16_t *yp = &sm.v[tq][32 * g][col];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = own ? Sg[(long long)i * A.V] : 0.f;
-        put_state(false);
-
-        const int chunks = (w.len + DC_C - 1) / DC_C;
-        for (int c = 0; c < chunks; ++c, ++n) {
-            const int st = n % DC_KV, tp = n % DC_TP;
-            const int left = w.len - c * DC_C;
-            const float s_old = sS;
-            float x[32];
-            float mr = 0.f, unused = 0.f, mul, sR;
-            // R
-            dc_wait(A, sm, &sm.b_tp[tp], (n / DC_TP) & 1);
+            for (int i = 0; i < 8; ++i) {
+                const Four fq = lds_four(sm.fqs[tq] + 32 * g + 4 * i), fp = lds_four(sm.fp[tq] + 32 * g + 4 * i);
+                const float2 y0 = __ffma2_rn(__fmul2_rn(fq.a, two(s_old)), q[2 * i], __fmul2_rn(__fmul2_rn(fp.a, two(sU)), x[2 * i]));
+                const float2 y1 = __ffma2_rn(__fmul2_rn(fq.b, two(s_old)), q[2 * i + 1],
+                                             __fmul2_rn(__fmul2_rn(fp.b, two(sU)), x[2 * i + 1]));
+                const uint32_t p0 = pack2(y0.x, y0.y, (const T *)nullptr), p1 = pack2(y1.x, y1.y, (const T *)nullptr);
+                yp[(4 * i) * DC_VW] = (uint16_t)p0;
+                yp[(4 * i + 1) * DC_VW] = (uint16_t)(p0 >> 16);
+                yp[(4 * i + 2) * DC_VW] = (uint16_t)p1;
+                yp[(4 * i + 3) * DC_VW] = (uint16_t)(p1 >> 16);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            warp_arrive(&sm.b_out[tq]);
+        }
+        if (!w.there) break;
+        pending = true;
+        float2 x[16];
+        float mul;
+        // R
+        {
+            float m = 0.f, unused = 0.f, sR;
+            dc_wait(A, sm, &sm.b_v[tp], (n / 2) & 1);
+            dc_wait(A, sm, &sm.b_tp[tp], (n / 2) & 1);
             dc_wait(A, sm, &sm.b_KS, n & 1);
             tc_fence_after();
-            tmem_ld32(tm + TM_A + 32 * g, x);
+            tmem_ld32(tm + TM_A + 32 * g, reinterpret_cast<float *>(x));
             tmem_ld_wait();
+            const uint16_t *vp = &sm.v[tp][32 * g][col];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = 32 * g + i;
-                const uint16_t raw = own ? sm.v[st][t][col] : (uint16_t)0;
-                const float2 v = unpack2(raw, (const T *)nullptr);
-                x[i] = fmaf(-sm.fks[tp][t], sS * x[i], sm.fv[tp][t] * v.x);
-                mr = fmaxf(mr, fabsf(x[i]));
+            for (int i = 0; i < 8; ++i) {
+                const Four fk = lds_four(sm.fks[tp] + 32 * g + 4 * i), fv = lds_four(sm.fv[tp] + 32 * g + 4 * i);
+                float2 v0 = make_float2(unpack2(vp[(4 * i) * DC_VW], (const T *)nullptr).x,
+                                        unpack2(vp[(4 * i + 1) * DC_VW], (const T *)nullptr).x);
+                float2 v1 = make_float2(unpack2(vp[(4 * i + 2) * DC_VW], (const T *)nullptr).x,
+                                        unpack2(vp[(4 * i + 3) * DC_VW], (const T *)nullptr).x);
+                x[2 * i] = __ffma2_rn(__fmul2_rn(x[2 * i], two(-sS)), fk.a, __fmul2_rn(fv.a, v0));
+                x[2 * i + 1] = __ffma2_rn(__fmul2_rn(x[2 * i + 1], two(-sS)), fk.b, __fmul2_rn(fv.b, v1));
+                m = max3(max3(m, x[2 * i]), x[2 * i + 1]);
             }
-            both(mr, unused);
-            pow2_scale(mr, mul, sR);
-            {
-                uint32_t hi[16], lo[16];
+            if (!own) {  // columns past the value dimension: what lies there is nobody's
+                m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split2(x[2 * i] * mul, x[2 * i + 1] * mul, hi[i], lo[i]);
-                tmem_st16(tm + TM_R + 16 * g, hi);
-                tmem_st16(tm + TM_R + 32 + 16 * g, lo);
+                for (int i = 0; i < 16; ++i) x[i] = two(0.f);
             }
+            both(m, unused);
+            pow2_scale(m, mul, sR);
+            put(x, mul, tm + TM_R + 16 * g, tm + TM_R + 32 + 16 * g);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&sm.b_R);
-            // U, and U as the state takes it
+            sU = sR;
+        }
+        // U, and U as the state takes it (U~)
+        {
+            float mu = 0.f, mw = 0.f, mulw;
+            const float sR = sU;
             dc_wait(A, sm, &sm.b_U, n & 1);
             tc_fence_after();
-            tmem_ld32(tm + TM_A + 32 * g, x);
+            tmem_ld32(tm + TM_A + 32 * g, reinterpret_cast<float *>(x));
             tmem_ld_wait();
-            float mu = 0.f, mw = 0.f, sU, sW, mulw;
+            float2 y[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = 32 * g + i;
-                x[i] *= sR * sm.fu[tp][t];
-                mu = fmaxf(mu, fabsf(x[i]));
-                mw = fmaxf(mw, fabsf(x[i] * sm.fw[tp][t]));
+            for (int i = 0; i < 8; ++i) {
+                const Four fu = lds_four(sm.fu[tp] + 32 * g + 4 * i), fw = lds_four(sm.fw[tp] + 32 * g + 4 * i);
+                x[2 * i] = __fmul2_rn(__fmul2_rn(x[2 * i], two(sR)), fu.a);
+                x[2 * i + 1] = __fmul2_rn(__fmul2_rn(x[2 * i + 1], two(sR)), fu.b);
+                y[2 * i] = __fmul2_rn(x[2 * i], fw.a);
+                y[2 * i + 1] = __fmul2_rn(x[2 * i + 1], fw.b);
+                mu = max3(max3(mu, x[2 * i]), x[2 * i + 1]);
+                mw = max3(max3(mw, y[2 * i]), y[2 * i + 1]);
             }
             both(mu, mw);
             pow2_scale(mu, mul, sU);
             pow2_scale(mw, mulw, sW);
             dc_wait(A, sm, &sm.b_QS, n & 1);  // S's parts have been read
             tc_fence_after();
-            {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 32 * g + 2 * i;
-                    split2(x[2 * i] * sm.fw[tp][t] * mulw, x[2 * i + 1] * sm.fw[tp][t + 1] * mulw, hi[i], lo[i]);
-                }
-                tmem_st16(tm + TM_S + 16 * g, hi);
-                tmem_st16(tm + TM_S + 32 + 16 * g, lo);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split2(x[2 * i] * mul, x[2 * i + 1] * mul, hi[i], lo[i]);
-                tmem_st16(tm + TM_S + 64 + 16 * g, hi);
-                if (LO) tmem_st16(tm + TM_S + 96 + 16 * g, lo);
-            }
+            put(y, mulw, tm + TM_S + 16 * g, tm + TM_S + 32 + 16 * g);
+            put(x, mul, tm + TM_S + 64 + 16 * g, tm + TM_S + 96 + 16 * g);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&sm.b_W);
-            // the new state
-            const float gC = sm.gC[tp];
-            dc_wait(A, sm, &sm.b_D, n & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                tmem_ld32(tm + TM_A + 64 * g + 32 * b, x);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(sW, x[i], gC * S[32 * b + i]);
-            }
-            ++n;
-            if (c + 1 < chunks)
-                put_state(true);
-            else
-                dc_wait(A, sm, &sm.b_PU, (n - 1) & 1);
-            --n;
-            // the outputs, while the next chunk's K S runs
-            tc_fence_after();
-            float q[32];
-            tmem_ld32(tm + TM_Q + 32 * g, q);
-            tmem_ld32(tm + TM_PU + 32 * g, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int t = 32 * g + i;
-                x[i] = fmaf(s_old * sm.fqs[tp][t], q[i], sU * sm.fp[tp][t] * x[i]);
-            }
-            tc_fence_before();
-            warp_arrive(&sm.b_out[tp]);
-            if (own) {
-                T *yp = static_cast<T *>(A.y) + (w.first + (long long)c * DC_C + 32 * g) * A.y_stride + (long long)w.h * A.V + vcol;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (32 * g + i < left) store1(yp + i * A.y_stride, x[i]);
-            }
         }
-        if (own) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) Sg[(long long)i * A.V] = S[i];
-        }
-        ++w.round;
-        dc_fetch(A, sm, w);
     }
 }
 
@@ -853,7 +1018,7 @@ __device__ __forceinline__ void dc_order(const DeltaArgs &A, DcSmem &sm)
     }
 }
 
-template <class T, bool LO>
+template <class T>
 __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaArgs A)
 {
     extern __shared__ __align__(1024) unsigned char raw_smem[];
@@ -866,23 +1031,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (threadIdx.x == 0) {
         sm.stop = 0;
         for (int i = 0; i < DC_KV; ++i) {
-            mbar_init(&sm.b_kq[i], DC_PREP / 32);
+            mbar_init(&sm.b_ld[i], 1);
             mbar_init(&sm.b_free[i], 1);
+            mbar_init(&sm.b_kq[i], DC_PREP / 32);
         }
-        for (int i = 0; i < DC_TP; ++i) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.b_v[i], 1);
+            mbar_init(&sm.b_vfree[i], 1);
+            mbar_init(&sm.b_sc[i], 1);
             mbar_init(&sm.b_tp[i], DC_PREP / 32);
             mbar_init(&sm.b_out[i], DC_CHAIN / 32);
         }
         mbar_init(&sm.b_S, DC_CHAIN / 32);
         mbar_init(&sm.b_R, DC_CHAIN / 32);
         mbar_init(&sm.b_W, DC_CHAIN / 32);
-        mbar_init(&sm.b_KS, 1);
-        mbar_init(&sm.b_QS, 1);
-        mbar_init(&sm.b_U, 1);
-        mbar_init(&sm.b_D, 1);
-        mbar_init(&sm.b_PU, 1);
-        mbar_init(&sm.b_KK, 1);
-        mbar_init(&sm.b_end, 1);
+        for (uint64_t *b : {&sm.b_KS, &sm.b_QS, &sm.b_U, &sm.b_D, &sm.b_PU, &sm.b_KK, &sm.b_end}) mbar_init(b, 1);
         mbar_fence_init();
     }
     dc_order(A, sm);
@@ -892,13 +1055,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     const uint32_t tmem = sm.taddr;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(DC_REG_CHAIN));
-        dc_chain<T, LO>(A, sm, tmem);
+        dc_chain<T>(A, sm, tmem);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(DC_REG_PREP));
-        dc_prep<T, LO>(A, sm, tmem);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_PREP));
+        dc_prep<T>(A, sm, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_ISSUE));
-        if (threadIdx.x == DC_CHAIN + DC_PREP) dc_issue<LO>(A, sm, tmem);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_HELP));
+        if (warp == 12) {
+            if ((threadIdx.x & 31) == 0) dc_issue(A, sm, tmem);
+            __syncwarp();
+        } else if (warp == 13)
+            dc_store<T>(A, sm);
+        else if (warp == 14)
+            dc_scalars(A, sm);
+        else
+            dc_bring<T>(A, sm);
     }
     tc_fence_before();
     __syncthreads();
@@ -906,14 +1077,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-template <class T, bool LO>
+template <class T>
 cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
     const long long items = (long long)a.rows * a.H * ((a.V + DC_VW - 1) / DC_VW);
-    cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<T, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(DcSmem));
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<T, LO><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(a);
+    delta_chunk_kernel<T><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -926,8 +1097,8 @@ bool delta_chunk_fits(const DeltaArgs &a)
 
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
-    return a.dtype == SKETCHSSM_BF16 ? launch_type<__nv_bfloat16, true>(a, sms, stream)
-                                     : launch_type<__half, true>(a, sms, stream);
+    return a.dtype == SKETCHSSM_BF16 ? launch_type<__nv_bfloat16>(a, sms, stream)
+                                     : launch_type<__half>(a, sms, stream);
 }
 
 }  // namespace sk

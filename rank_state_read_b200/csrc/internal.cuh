@@ -135,7 +135,7 @@ struct DeltaArgs {
 };
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t stream);
 // prompts of 16-bit tokens, 64 at a time on the tensor cores
-constexpr int DC_MAX_SEQS = 2048;
+constexpr int DC_MAX_SEQS = 1024;
 bool delta_chunk_fits(const DeltaArgs &a);
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream);
 
