@@ -52,15 +52,15 @@ constexpr float DC_STRONG = 100.f;  // exponents of a chunk's decays within whic
 constexpr uint32_t TM_A = 0;     // K S^T, then U^T (64); with the next 64: the state's increment
 constexpr uint32_t TM_Q = 128;   // Q S^T (64)
 constexpr uint32_t TM_PU = 192;  // P U (64)
-constexpr uint32_t TM_S = 256;   // S hi, lo (64 each); then U~ hi, lo, U hi, lo (32 each)
-constexpr uint32_t TM_R = 384;   // R hi, lo (32 each)
+constexpr uint32_t TM_S = 256;   // S hi, lo (64 each); then U~ hi, lo (32 each)
+constexpr uint32_t TM_R = 384;   // R hi, lo (32 each); then U hi, lo
 constexpr uint32_t TM_KK = 448;  // [K; Q] K^T (64)
 
 struct DcSmem {
     // 1024-byte aligned operand tiles, rows of 128 bytes, 128-byte swizzle
     uint8_t kq[DC_KV][2][128 * 128];  // k dims 0-63 | 64-127; rows 0-63 k, 64-127 q
     uint8_t tp[2][4][64 * 128];       // T hi, T lo, P hi, P lo
-    float m[64 * 64];                 // A, then T, in fp32
+    float m[64][68];                  // A, then T, in fp32
     uint16_t v[2][DC_C][DC_VW];       // values, then outputs
     // per token: factors of v and K S in R; of U; of U for the state; of Q S; of P U
     float fv[2][DC_C], fks[2][DC_C], fu[2][DC_C], fw[2][DC_C], fqs[2][DC_C], fp[2][DC_C];
@@ -181,7 +181,13 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
     lo = h2_bits(__float22half2_rn(__ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), v)));
 }
 
-__device__ __forceinline__ float max3(float m, float2 v) { return fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))); }
+// max(m, |v.x|, |v.y|), m not negative
+__device__ __forceinline__ float max3(float m, float2 v)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(v.x), "f"(v.y));
+    return r;
+}
 
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 
@@ -205,7 +211,8 @@ __device__ __forceinline__ float ex2(float x)
 // ---- which chunk comes next ----
 
 static_assert(sizeof(DcSmem) <= 232448, "shared memory of one CTA");
-static_assert(offsetof(DcSmem, kq) % 1024 == 0 && offsetof(DcSmem, tp) % 1024 == 0, "swizzled tiles");
+static_assert(offsetof(DcSmem, kq) % 1024 == 0 && offsetof(DcSmem, tp) % 1024 == 0 &&
+                  offsetof(DcSmem, m) == offsetof(DcSmem, tp) + sizeof(DcSmem::tp), "swizzled tiles");
 static_assert(offsetof(DcSmem, m) % 16 == 0 && offsetof(DcSmem, v) % 16 == 0 && offsetof(DcSmem, fv) % 16 == 0 &&
                   offsetof(DcSmem, beta) % 16 == 0 && offsetof(DcSmem, col) % 16 == 0 && offsetof(DcSmem, b_ld) % 8 == 0,
               "vector accesses");
@@ -284,13 +291,26 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// ---- warp 15: q, k, v of one chunk after the other, a row of 256 (128) bytes a copy; a row of
-// k or q lands unswizzled (the conversion reads it so) ----
+// ---- warp 15: q, k, v of one chunk after the other, 16 bytes a lane ----
 
+// cp.async of 16 bytes, or 16 zero bytes
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// an arrival of this thread on `bar` once its copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// (A row of 128 or 256 bytes a bulk copy costs the copy engine some 60 cycles: 320 rows a chunk were
+// more than the chunk's products.)
 template <class T>
 __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = lane & 15, r0 = lane >> 4;  // 16 lanes a row, 2 rows a pass
     DcWalk w;
     dc_start(w);
     for (int n = 0;; ++n) {
@@ -298,32 +318,39 @@ __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm)
         if (!w.there) break;
         const int st = n % DC_KV, sv = n & 1;
         const long long t0 = w.first + w.chunk * DC_C;
-        const int rows = min(w.len - w.chunk * DC_C, DC_C);
+        const int left = w.len - w.chunk * DC_C;
         const int hq = w.h / A.hpq;
-        const uint32_t vb = (uint32_t)min(DC_VW, A.V - w.slice * DC_VW) * 2;
         if (n >= DC_KV) dc_wait(A, sm, &sm.b_free[st], (n / DC_KV - 1) & 1);
-        if (lane == 0) mbar_arrive_expect_tx(&sm.b_ld[st], (uint32_t)rows * 512);
-        __syncwarp();
-        for (int t = lane; t < rows; t += 32) {
-            const T *k = static_cast<const T *>(A.k) + (t0 + t) * A.k_stride + hq * KDIM;
-            const T *q = static_cast<const T *>(A.q) + (t0 + t) * A.q_stride + hq * KDIM;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                bulk_copy_g2s(sm.kq[st][i] + t * 128, k + 64 * i, 128, &sm.b_ld[st]);
-                bulk_copy_g2s(sm.kq[st][i] + (64 + t) * 128, q + 64 * i, 128, &sm.b_ld[st]);
+        {
+            const T *k = static_cast<const T *>(A.k) + t0 * A.k_stride + hq * KDIM + c * 8;
+            const T *q = static_cast<const T *>(A.q) + t0 * A.q_stride + hq * KDIM + c * 8;
+            const uint32_t dst = smem_addr(sm.kq[st][c >> 3]);
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int t = 2 * i + r0;
+                const bool there = t < left;
+                const uint32_t at = dst + t * 128 + (((c ^ t) & 7) << 4);
+                cp_async16_zfill(at, there ? k + t * A.k_stride : k, there);
+                cp_async16_zfill(at + 64 * 128, there ? q + t * A.q_stride : q, there);
             }
+            cp_async_arrive(&sm.b_ld[st]);
         }
         if (n >= 2) dc_wait(A, sm, &sm.b_vfree[sv], (n / 2 - 1) & 1);
-        // rows past the sequence's end count as zeros
-        for (int i = rows * (DC_VW / 8) + lane; i < DC_C * (DC_VW / 8); i += 32)
-            *reinterpret_cast<uint4 *>(&sm.v[sv][i / (DC_VW / 8)][i % (DC_VW / 8) * 8]) = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&sm.b_v[sv], (uint32_t)rows * vb);
-        __syncwarp();
-        for (int t = lane; t < rows; t += 32)
-            bulk_copy_g2s(sm.v[sv][t], static_cast<const T *>(A.v) + (t0 + t) * A.v_stride + (long long)w.h * A.V + w.slice * DC_VW,
-                          vb, &sm.b_v[sv]);
+        {
+            const T *v = static_cast<const T *>(A.v) + t0 * A.v_stride + (long long)w.h * A.V + w.slice * DC_VW + c * 8;
+            if (w.slice * DC_VW + c * 8 < A.V) {
+#pragma unroll 4
+                for (int i = 0; i < 32; ++i) {
+                    const int t = 2 * i + r0;
+                    const bool there = t < left;
+                    cp_async16_zfill(smem_addr(&sm.v[sv][t][c * 8]), there ? v + t * A.v_stride : v, there);
+                }
+            }
+            cp_async_arrive(&sm.b_v[sv]);
+        }
     }
+    cp_async_commit();
+    cp_async_wait<0>();
 }
 
 // ---- warp 13: outputs, from the place of their chunk's values ----
@@ -331,28 +358,27 @@ __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm)
 template <class T>
 __device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = lane & 15, r0 = lane >> 4;
     DcWalk w;
     dc_start(w);
     for (int n = 0;; ++n) {
         dc_next(A, sm, w);
         if (!w.there) break;
         const int sv = n & 1;
-        const long long t0 = w.first + w.chunk * DC_C;
-        const int rows = min(w.len - w.chunk * DC_C, DC_C);
-        const uint32_t vb = (uint32_t)min(DC_VW, A.V - w.slice * DC_VW) * 2;
+        const int left = w.len - w.chunk * DC_C;
+        T *y = static_cast<T *>(A.y) + (long long)(w.first + w.chunk * DC_C) * A.y_stride + (long long)w.h * A.V +
+               w.slice * DC_VW + c * 8;
         dc_wait(A, sm, &sm.b_out[sv], (n / 2) & 1);
-        for (int t = lane; t < rows; t += 32) {
-            T *y = static_cast<T *>(A.y) + (t0 + t) * A.y_stride + (long long)w.h * A.V + w.slice * DC_VW;
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(y), "r"(smem_addr(sm.v[sv][t])),
-                         "r"(vb)
-                         : "memory");
+        if (w.slice * DC_VW + c * 8 < A.V) {
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int t = 2 * i + r0;
+                if (t < left)
+                    *reinterpret_cast<uint4 *>(y + t * A.y_stride) = *reinterpret_cast<const uint4 *>(&sm.v[sv][t][c * 8]);
+            }
         }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         warp_arrive(&sm.b_vfree[sv]);
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- warp 14: the decays of a chunk's tokens, two tokens a lane ----
@@ -439,9 +465,6 @@ __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
 
 // ---- warps 8-11 ----
 
-// where A and T lie in fp32: rows of 64 floats, 16-byte chunks permuted by the row
-__device__ __forceinline__ int tri(int i, int j) { return i * 64 + ((((j >> 2) ^ i) & 15) << 2) + (j & 3); }
-
 __device__ __forceinline__ float tf32_round(float x)
 {
     uint32_t r;
@@ -458,28 +481,29 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], con
 }
 
 // L[16 MT x 8 KT] B[8 KT x 8] as MT tiles of 16 rows x 8 columns, three tf32 products each (in
-// accumulators of their own, so that none waits for another): fp32 accuracy.  l(i, k), b(k, n):
-// the operands' elements.
-template <int MT, int KT, class FL, class FB>
+// accumulators of their own, so that none waits for another): fp32 accuracy.  l(m, i, k): L at
+// row i + lane / 4, column k + lane % 4; b(k): B at row k + lane % 4, column lane / 4; LOWER: L is
+// lower triangular.
+template <int MT, int KT, bool LOWER = false, class FL, class FB>
 __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float d1[MT][4] = {}, d2[MT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < KT; ++ks) {
         float bh[2], bl[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float x = b(8 * ks + t + 4 * e, g);
+            const float x = b(8 * ks + 4 * e);
             bh[e] = tf32_round(x);
             bl[e] = x - bh[e];
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+            if (LOWER && 8 * ks >= 16 * (m + 1)) continue;
             float ah[4], al[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = l(16 * m + g + 8 * (e & 1), 8 * ks + t + 4 * (e >> 1));
+                const float x = l(m, 16 * m + 8 * (e & 1), 8 * ks + 4 * (e >> 1));
                 ah[e] = tf32_round(x);
                 al[e] = x - ah[e];
             }
@@ -498,81 +522,71 @@ __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
 // the group: the 16 x 16 blocks on the diagonal by substitution (a column a lane), then
 // T21 = -T22 A21 T11 for blocks of 16 and of 32.  Substitution in blocks is as stable as
 // substitution; the powers of A that a product form needs would not be.
-__device__ __forceinline__ void invert(float *M, float (&X)[32][36], int r)
+__device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], int r)
 {
     const int wq = r >> 5, lane = r & 31, g = lane >> 2, t = lane & 3;
     {
         const int o = 16 * wq, j = lane & 15;
+        const float *L = &M[o][o];
         float x[16];
         x[0] = j == 0 ? 1.f : 0.f;
 #pragma unroll
         for (int i = 1; i < 16; ++i) {
-            float s = 0.f;
+            // the newest value last: it is the one to wait for
+            float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
             for (int k4 = 0; k4 < i; k4 += 4) {
-                const float4 a = lds4(M + tri(o + i, o + k4));
-                s = fmaf(a.x, x[k4], s);
-                if (k4 + 1 < i) s = fmaf(a.y, x[k4 + 1], s);
-                if (k4 + 2 < i) s = fmaf(a.z, x[k4 + 2], s);
-                if (k4 + 3 < i) s = fmaf(a.w, x[k4 + 3], s);
+                const float4 a = lds4(L + i * 68 + k4);
+                s0 = fmaf(-a.x, x[k4], s0);
+                if (k4 + 1 < i) s1 = fmaf(-a.y, x[k4 + 1], s1);
+                if (k4 + 2 < i) s0 = fmaf(-a.z, x[k4 + 2], s0);
+                if (k4 + 3 < i) s1 = fmaf(-a.w, x[k4 + 3], s1);
             }
-            x[i] = (i == j ? 1.f : 0.f) - s;
+            x[i] = s0 + s1;
         }
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) M[tri(o + i, o + j)] = x[i];
+            for (int i = 0; i < 16; ++i) M[o + i][o + j] = x[i];
         }
     }
     named_sync(5, DC_PREP);
     {
         const int o = 32 * (wq >> 1), n0 = 8 * (wq & 1), xr = 16 * (wq >> 1);
+        const float *L21 = &M[o + 16 + g][o + t], *L22 = &M[o + 16 + g][o + 16 + t], *T11 = &M[o + t][o + n0 + g];
         float d[1][4] = {};
-        mul_tri<1, 2>(d, [&](int i, int k) { return M[tri(o + 16 + i, o + k)]; },
-                      [&](int k, int n) { return M[tri(o + k, o + n0 + n)]; });
+        mul_tri<1, 2>(d, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
+        float *x = &X[xr][n0];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) X[xr + g + 8 * (e >> 1)][n0 + 2 * t + (e & 1)] = d[0][e];
+        for (int e = 0; e < 4; ++e) x[(g + 8 * (e >> 1)) * 36 + 2 * t + (e & 1)] = d[0][e];
         __syncwarp();
         float f[1][4] = {};
-        mul_tri<1, 2>(f, [&](int i, int k) { return M[tri(o + 16 + i, o + 16 + k)]; },
-                      [&](int k, int n) { return X[xr + k][n0 + n]; });
+        mul_tri<1, 2>(f, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
         named_sync(5, DC_PREP);  // A21 has been read
 #pragma unroll
-        for (int e = 0; e < 4; ++e) M[tri(o + 16 + g + 8 * (e >> 1), o + n0 + 2 * t + (e & 1))] = -f[0][e];
+        for (int e = 0; e < 4; ++e) M[o + 16 + g + 8 * (e >> 1)][o + n0 + 2 * t + (e & 1)] = -f[0][e];
     }
     named_sync(5, DC_PREP);
     {
         const int n0 = 8 * wq;
+        const float *L21 = &M[32 + g][t], *L22 = &M[32 + g][32 + t], *T11 = &M[t][n0 + g];
         float d[2][4] = {};
-        mul_tri<2, 4>(d, [&](int i, int k) { return M[tri(32 + i, k)]; }, [&](int k, int n) { return M[tri(k, n0 + n)]; });
+        mul_tri<2, 4>(d, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
+        float *x = &X[0][n0];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) X[16 * m + g + 8 * (e >> 1)][n0 + 2 * t + (e & 1)] = d[m][e];
+            for (int e = 0; e < 4; ++e) x[(16 * m + g + 8 * (e >> 1)) * 36 + 2 * t + (e & 1)] = d[m][e];
         __syncwarp();
         float f[2][4] = {};
-        mul_tri<2, 4>(f, [&](int i, int k) { return M[tri(32 + i, 32 + k)]; }, [&](int k, int n) { return X[k][n0 + n]; });
+        mul_tri<2, 4, true>(f, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
         named_sync(5, DC_PREP);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) M[tri(32 + 16 * m + g + 8 * (e >> 1), n0 + 2 * t + (e & 1))] = -f[m][e];
+            for (int e = 0; e < 4; ++e) M[32 + 16 * m + g + 8 * (e >> 1)][n0 + 2 * t + (e & 1)] = -f[m][e];
     }
     named_sync(5, DC_PREP);
-}
-
-// 16 scaled values as fp16 parts into columns 16 c .. of row `t` of two swizzled tiles
-__device__ __forceinline__ void put16(uint8_t *hi, uint8_t *lo, int t, int c, const float2 (&x)[8], float mul)
-{
-    uint32_t h[8], l[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) split2(__fmul2_rn(x[e], two(mul)), h[e], l[e]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int off = t * 128 + (((2 * c + i) ^ (t & 7)) << 4);
-        *reinterpret_cast<uint4 *>(hi + off) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-        *reinterpret_cast<uint4 *>(lo + off) = make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
-    }
 }
 
 template <class T>
@@ -581,6 +595,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
     const int r = threadIdx.x - DC_CHAIN, wq = r >> 5;
     const int t = r & 63;        // token of this thread's row
     const bool is_q = r >= 64;
+    const int half = wq & 1;     // rows 32 half .. of k or q: the warp's
     const uint32_t kk = tmem + TM_KK + ((uint32_t)(wq * 32) << 16);
     DcWalk w;
     dc_start(w);
@@ -588,54 +603,43 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         dc_next(A, sm, w);
         if (!w.there) break;
         const int st = n % DC_KV, tp = n & 1;
-        const int left = w.len - w.chunk * DC_C;
         dc_wait(A, sm, &sm.b_ld[st], (n / DC_KV) & 1);
 
-        // this thread's row of k or q: its norm, and fp16 values at a power of two of their own,
-        // from plain to swizzled order (a half row at a time: position c takes what c ^ (r & 7) held)
+        // this thread's row of k or q: its norm, and fp16 values at a power of two of their own, in
+        // place (the 16-byte pieces in an order that keeps the row's lanes on different banks)
         float f_own;
         {
-            uint8_t *row[2] = {sm.kq[st][0] + r * 128, sm.kq[st][1] + r * 128};
+            uint8_t *row = sm.kq[st][0] + r * 128;
             const int sw = (r & 7) << 4;
-            const bool there = t < left;
-            float2 s2 = two(0.f);
+            float2 s2[2] = {two(0.f), two(0.f)};
             float m = 0.f;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll 4
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(row[hf] + ((c << 4) ^ sw));
-                    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+            for (int c = 0; c < 16; ++c) {
+                const uint4 raw = *reinterpret_cast<const uint4 *>(row + (c >> 3) * (128 * 128) + (((c & 7) << 4) ^ sw));
+                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2(v[e], (const T *)nullptr);
-                        s2 = __ffma2_rn(f, f, s2);
-                        m = max3(m, f);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack2(v[e], (const T *)nullptr);
+                    if (A.normalize) s2[e & 1] = __ffma2_rn(f, f, s2[e & 1]);
+                    m = max3(m, f);
                 }
+            }
             float mul, inv;
             pow2_scale(m, mul, inv);
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-                uint4 o[8];
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+                uint4 *at = reinterpret_cast<uint4 *>(row + (c >> 3) * (128 * 128) + (((c & 7) << 4) ^ sw));
+                const uint4 raw = *at;
+                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t o[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(row[hf] + ((c << 4) ^ sw));
-                    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
-                    uint32_t p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
-                        if (!there) p[e] = 0;
-                    }
-                    o[c] = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row[hf] + (c << 4)) = o[c];
+                for (int e = 0; e < 4; ++e)
+                    o[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
+                *at = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (A.normalize) inv *= rsqrtf(s2.x + s2.y + DELTA_QK_EPS);
-            if (is_q) inv *= A.scale;
-            f_own = there ? inv : 0.f;
+            const float2 s = __fadd2_rn(s2[0], s2[1]);
+            if (A.normalize) inv *= rsqrtf(s.x + s.y + DELTA_QK_EPS);
+            f_own = is_q ? inv * A.scale : inv;
         }
         dc_wait(A, sm, &sm.b_sc[tp], (n / 2) & 1);
         const bool strong = sm.strong[tp];
@@ -659,97 +663,91 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         float f = is_q ? f_own : f_own * beta;
         if (!strong) f *= sm.er[tp][t];
         const int last = is_q ? t : t - 1;
-        const float gh = sm.gh[tp][t], gl = sm.gl[tp][t];
-        // columns 16 c .. of this row of A or P
-        auto entries = [&](int c, float2 (&x)[8]) {
-            tmem_ld16n(kk + 16 * c, reinterpret_cast<float *>(x));
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Four cf = lds_four(sm.col + 16 * c + 4 * e);
-                x[2 * e] = __fmul2_rn(__fmul2_rn(x[2 * e], cf.a), two(f));
-                x[2 * e + 1] = __fmul2_rn(__fmul2_rn(x[2 * e + 1], cf.b), two(f));
-            }
-            if (strong) {
-                // the chunk forgets so much that the factors of its decays leave fp32's range
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = 16 * c + 2 * e;
-                    x[e].x *= ex2((gh - sm.gh[tp][j]) + (gl - sm.gl[tp][j]));
-                    x[e].y *= ex2((gh - sm.gh[tp][j + 1]) + (gl - sm.gl[tp][j + 1]));
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (16 * c + 2 * e > last) x[e].x = 0.f;
-                if (16 * c + 2 * e + 1 > last) x[e].y = 0.f;
-            }
-        };
+        // this row of A or P; rows below 32 have zeros right of column 32, which stay from the start
+        float2 x[32];
         dc_wait(A, sm, &sm.b_KK, n & 1);
         tc_fence_after();
-        if (!is_q) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                float2 x[8];
-                entries(c, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    st4(sm.m + tri(t, 16 * c + 4 * e), make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y));
+        for (int c = 0; c < 4; ++c) {
+            if (c < 2 * half + 2) {
+                tmem_ld16n(kk + 16 * c, reinterpret_cast<float *>(x + 8 * c));
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Four cf = lds_four(sm.col + 16 * c + 4 * e);
+                    x[8 * c + 2 * e] = __fmul2_rn(__fmul2_rn(x[8 * c + 2 * e], cf.a), two(f));
+                    x[8 * c + 2 * e + 1] = __fmul2_rn(__fmul2_rn(x[8 * c + 2 * e + 1], cf.b), two(f));
+                }
+                if (c >= 2 * half) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (16 * c + 2 * e > last) x[8 * c + e].x = 0.f;
+                        if (16 * c + 2 * e + 1 > last) x[8 * c + e].y = 0.f;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[8 * c + e] = two(0.f);
             }
         }
-        // this stage of T, P and their factors is free once the chunk two before has given its outputs
-        if (n >= 2) dc_wait(A, sm, &sm.b_out[tp], (n / 2 - 1) & 1);
-        if (is_q) {
-            float m = 0.f, mul, inv;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                float2 x[8];
-                entries(c, x);
+        if (strong) {
+            // the chunk forgets so much that the factors of its decays leave fp32's range
+            const float gh = sm.gh[tp][t], gl = sm.gl[tp][t];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = max3(m, x[e]);
+            for (int e = 0; e < 32; ++e) {
+                if (2 * e <= last) x[e].x *= ex2((gh - sm.gh[tp][2 * e]) + (gl - sm.gl[tp][2 * e]));
+                if (2 * e + 1 <= last) x[e].y *= ex2((gh - sm.gh[tp][2 * e + 1]) + (gl - sm.gl[tp][2 * e + 1]));
             }
-            pow2_scale(m, mul, inv);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                float2 x[8];
-                entries(c, x);
-                put16(sm.tp[tp][2], sm.tp[tp][3], t, c, x, mul);
-            }
-            sm.fp[tp][t] = inv;
-            sm.fqs[tp][t] = dec * f_own;
-        } else {
-            sm.fv[tp][t] = beta;
-            sm.fks[tp][t] = beta * dec * f_own;
-            sm.fw[tp][t] = sm.rest[tp][t] * f_own;
-            if (t == 63) sm.gC[tp] = dec;
+        }
+        if (!is_q) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e < 8 * half + 8) st4(&sm.m[t][4 * e], make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y));
         }
         named_sync(5, DC_PREP);
         invert(sm.m, sm.x, r);
         if (!is_q) {
-            float m = 0.f, mul, inv;
-#pragma unroll 4
-            for (int j4 = 0; j4 < 64; j4 += 4) {
-                const Four v = lds_four(sm.m + tri(t, j4));
-                m = max3(max3(m, v.a), v.b);
-            }
-            pow2_scale(m, mul, inv);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                float2 x[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Four v = lds_four(sm.m + tri(t, 16 * c + 4 * e));
+            for (int e = 0; e < 16; ++e)
+                if (e < 8 * half + 8) {
+                    const Four v = lds_four(&sm.m[t][4 * e]);
                     x[2 * e] = v.a;
                     x[2 * e + 1] = v.b;
                 }
-                put16(sm.tp[tp][0], sm.tp[tp][1], t, c, x, mul);
+        }
+        // this stage of T, P and their factors is free once the chunk two before has given its outputs
+        if (n >= 2) dc_wait(A, sm, &sm.b_out[tp], (n / 2 - 1) & 1);
+        {
+            float m = 0.f, mul, inv;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) m = max3(m, x[e]);
+            pow2_scale(m, mul, inv);
+            uint8_t *hi = sm.tp[tp][is_q ? 2 : 0] + t * 128, *lo = hi + 64 * 128;
+            const int sw = (t & 7) << 4;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (c < 4 * half + 4) {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2(__fmul2_rn(x[4 * c + e], two(mul)), h[e], l[e]);
+                    *reinterpret_cast<uint4 *>(hi + ((c << 4) ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(lo + ((c << 4) ^ sw)) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
             }
-            sm.fu[tp][t] = inv;
+            if (is_q) {
+                sm.fp[tp][t] = inv;
+                sm.fqs[tp][t] = dec * f_own;
+            } else {
+                sm.fu[tp][t] = inv;
+                sm.fv[tp][t] = beta;
+                sm.fks[tp][t] = beta * dec * f_own;
+                sm.fw[tp][t] = sm.rest[tp][t] * f_own;
+                if (t == 63) sm.gC[tp] = dec;
+            }
         }
         fence_async_smem();
         tc_fence_before();
         warp_arrive(&sm.b_tp[tp]);
-        named_sync(5, DC_PREP);  // T in fp32 has been read
     }
 }
 
@@ -776,13 +774,6 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         for (int i = 0; i < 16; ++i)
             mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
         umma_commit(&sm.b_KS);
-        // Q S, once the chunk before has read its own
-        if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) & 1], ((n - 1) / 2) & 1);
-        tc_fence_after();
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i)
-            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_QS);
         // U = T R: (R lo, T hi), (R hi, T lo), (R hi, T hi)
         dc_wait(A, sm, &sm.b_R, n & 1);
         tc_fence_after();
@@ -791,6 +782,13 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
             mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
                    i > 0);
         umma_commit(&sm.b_U);
+        // Q S, in the shadow of what U goes through next, once the chunk before has read its own
+        if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) & 1], ((n - 1) / 2) & 1);
+        tc_fence_after();
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i)
+            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+        umma_commit(&sm.b_QS);
         // the state's increment: k as the right operand, tokens along K
         dc_wait(A, sm, &sm.b_W, n & 1);
         tc_fence_after();
@@ -802,7 +800,7 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         // P U: (U lo, P hi), (U hi, P lo), (U hi, P hi)
 #pragma unroll 4
         for (int i = 0; i < 12; ++i)
-            mma_ts(tmem + TM_PU, tmem + TM_S + 64 + (i < 4 ? 32 : 0) + 8 * (i & 3),
+            mma_ts(tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
                    t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
         umma_commit(&sm.b_PU);
     }
@@ -881,7 +879,6 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
                 S[i].y = own ? Sg[(long long)(2 * i + 1) * A.V] : 0.f;
             }
         }
-        if (pending) dc_wait(A, sm, &sm.b_PU, (n - 1) & 1);  // nothing reads U's parts any more
         s_old = sS;
         if (w.there) {
             float m = 0.f, unused = 0.f, mul;
@@ -898,6 +895,7 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
         }
         if (pending) {
             // the outputs of the chunk before, while this one's K S runs: into the place of its values
+            dc_wait(A, sm, &sm.b_PU, (n - 1) & 1);
             tc_fence_after();
             float2 q[16], x[16];
             tmem_ld32(tm + TM_Q + 32 * g, reinterpret_cast<float *>(q));
@@ -916,7 +914,6 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
                 yp[(4 * i + 2) * DC_VW] = (uint16_t)p1;
                 yp[(4 * i + 3) * DC_VW] = (uint16_t)(p1 >> 16);
             }
-            fence_async_smem();
             tc_fence_before();
             warp_arrive(&sm.b_out[tq]);
         }
@@ -970,8 +967,8 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const Four fu = lds_four(sm.fu[tp] + 32 * g + 4 * i), fw = lds_four(sm.fw[tp] + 32 * g + 4 * i);
-                x[2 * i] = __fmul2_rn(__fmul2_rn(x[2 * i], two(sR)), fu.a);
-                x[2 * i + 1] = __fmul2_rn(__fmul2_rn(x[2 * i + 1], two(sR)), fu.b);
+                x[2 * i] = __fmul2_rn(x[2 * i], fu.a);  // in units of sR
+                x[2 * i + 1] = __fmul2_rn(x[2 * i + 1], fu.b);
                 y[2 * i] = __fmul2_rn(x[2 * i], fw.a);
                 y[2 * i + 1] = __fmul2_rn(x[2 * i + 1], fw.b);
                 mu = max3(max3(mu, x[2 * i]), x[2 * i + 1]);
@@ -980,10 +977,12 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
             both(mu, mw);
             pow2_scale(mu, mul, sU);
             pow2_scale(mw, mulw, sW);
+            sU *= sR;
+            sW *= sR;
+            put(x, mul, tm + TM_R + 16 * g, tm + TM_R + 32 + 16 * g);
             dc_wait(A, sm, &sm.b_QS, n & 1);  // S's parts have been read
             tc_fence_after();
             put(y, mulw, tm + TM_S + 16 * g, tm + TM_S + 32 + 16 * g);
-            put(x, mul, tm + TM_S + 64 + 16 * g, tm + TM_S + 96 + 16 * g);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&sm.b_W);
@@ -1031,12 +1030,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (threadIdx.x == 0) {
         sm.stop = 0;
         for (int i = 0; i < DC_KV; ++i) {
-            mbar_init(&sm.b_ld[i], 1);
+            mbar_init(&sm.b_ld[i], 32);
             mbar_init(&sm.b_free[i], 1);
             mbar_init(&sm.b_kq[i], DC_PREP / 32);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.b_v[i], 1);
+            mbar_init(&sm.b_v[i], 32);
             mbar_init(&sm.b_vfree[i], 1);
             mbar_init(&sm.b_sc[i], 1);
             mbar_init(&sm.b_tp[i], DC_PREP / 32);
@@ -1048,6 +1047,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
         for (uint64_t *b : {&sm.b_KS, &sm.b_QS, &sm.b_U, &sm.b_D, &sm.b_PU, &sm.b_KK, &sm.b_end}) mbar_init(b, 1);
         mbar_fence_init();
     }
+    // what stays zero: T and P right of column 32 in rows below 32, A there
+    for (int i = threadIdx.x; i < (int)(sizeof(sm.tp) + sizeof(sm.m)) / 16; i += DC_THREADS)
+        reinterpret_cast<uint4 *>(sm.tp)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
     dc_order(A, sm);
     tc_fence_before();
     __syncthreads();
