@@ -95,22 +95,38 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr, uint32_t lbo, uin
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The whole warp runs the code around an MMA and one lane (`leads`) issues it: addresses and
+// descriptors then stay in uniform registers (an MMA every 32 cycles at N = 64; 47 from a branch
+// that one lane takes).
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t leads, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leads)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ss(uint32_t leads, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leads)
         : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t leads, uint64_t *bar)
+{
+    if (leads) umma_commit(bar);
+    __syncwarp();
 }
 
 // 32 columns of the warp's 32 lanes; tmem_ld_wait before the values are used
@@ -589,6 +605,14 @@ __device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], i
     named_sync(5, DC_PREP);
 }
 
+// largest magnitude of 8 packed values
+__device__ __forceinline__ float max_of(uint4 v, const __nv_bfloat16 *)
+{
+    auto a = [](uint32_t w) { return __habs2(*reinterpret_cast<__nv_bfloat162 *>(&w)); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(a(v.x), a(v.y)), __hmax2(a(v.z), a(v.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 template <class T>
 __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
@@ -597,6 +621,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
     const bool is_q = r >= 64;
     const int half = wq & 1;     // rows 32 half .. of k or q: the warp's
     const uint32_t kk = tmem + TM_KK + ((uint32_t)(wq * 32) << 16);
+    const uint32_t leads = elect_lane();
     DcWalk w;
     dc_start(w);
     for (int n = 0;; ++n) {
@@ -605,41 +630,65 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         const int st = n % DC_KV, tp = n & 1;
         dc_wait(A, sm, &sm.b_ld[st], (n / DC_KV) & 1);
 
-        // this thread's row of k or q: its norm, and fp16 values at a power of two of their own, in
-        // place (the 16-byte pieces in an order that keeps the row's lanes on different banks)
-        float f_own;
+        // this thread's row of k or q: its norm, and (bf16) fp16 values at a power of two of their
+        // own, in place.  The 16-byte pieces go in an order that keeps the row's lanes on
+        // different banks.  fp16 rows are operands as they are.
+        float f_own = 1.f;
         {
+            constexpr bool CONVERT = sizeof(T) == 2 && !__is_same(T, __half);
             uint8_t *row = sm.kq[st][0] + r * 128;
             const int sw = (r & 7) << 4;
-            float2 s2[2] = {two(0.f), two(0.f)};
-            float m = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                const uint4 raw = *reinterpret_cast<const uint4 *>(row + (c >> 3) * (128 * 128) + (((c & 7) << 4) ^ sw));
-                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+            float2 s2[4] = {two(0.f), two(0.f), two(0.f), two(0.f)};
+            float m = 0.f, mul = 1.f;
+            if (CONVERT || A.normalize) {
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint4 raw[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack2(v[e], (const T *)nullptr);
-                    if (A.normalize) s2[e & 1] = __ffma2_rn(f, f, s2[e & 1]);
-                    m = max3(m, f);
+                    for (int c = 0; c < 8; ++c)
+                        raw[c] = *reinterpret_cast<const uint4 *>(row + hf * (128 * 128) + ((c << 4) ^ sw));
+                    if constexpr (CONVERT) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) m = fmaxf(m, max_of(raw[c], (const T *)nullptr));
+                    }
+                    if (A.normalize) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = unpack2(v[e], (const T *)nullptr);
+                                s2[e] = __ffma2_rn(f, f, s2[e]);
+                            }
+                        }
+                    }
                 }
             }
-            float mul, inv;
-            pow2_scale(m, mul, inv);
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                uint4 *at = reinterpret_cast<uint4 *>(row + (c >> 3) * (128 * 128) + (((c & 7) << 4) ^ sw));
-                const uint4 raw = *at;
-                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
-                uint32_t o[4];
+            if constexpr (CONVERT) {
+                pow2_scale(m, mul, f_own);
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint4 raw[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
-                *at = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int c = 0; c < 8; ++c)
+                        raw[c] = *reinterpret_cast<const uint4 *>(row + hf * (128 * 128) + ((c << 4) ^ sw));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
+                        *reinterpret_cast<uint4 *>(row + hf * (128 * 128) + ((c << 4) ^ sw)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
             }
-            const float2 s = __fadd2_rn(s2[0], s2[1]);
-            if (A.normalize) inv *= rsqrtf(s.x + s.y + DELTA_QK_EPS);
-            f_own = is_q ? inv * A.scale : inv;
+            if (A.normalize) {
+                const float2 s = __fadd2_rn(__fadd2_rn(s2[0], s2[1]), __fadd2_rn(s2[2], s2[3]));
+                f_own *= rsqrtf(s.x + s.y + DELTA_QK_EPS);
+            }
+            if (is_q) f_own *= A.scale;
         }
         dc_wait(A, sm, &sm.b_sc[tp], (n / 2) & 1);
         const bool strong = sm.strong[tp];
@@ -648,17 +697,17 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         tc_fence_before();
         named_sync(5, DC_PREP);
         warp_arrive(&sm.b_kq[st]);
-        if (r == 0) {
+        if (wq == 0) {
             tc_fence_after();
-            const uint32_t idesc = idesc_f16(128, 64, false);
-#pragma unroll 1
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t d = sdesc_sw128(smem_addr(sm.kq[st][ks >> 2]) + (ks & 3) * 32, 16, 1024);
-                mma_ss(tmem + TM_KK, d, d, idesc, ks > 0);
+            constexpr uint32_t idesc = idesc_f16(128, 64, false);
+            const uint64_t d = sdesc_sw128(smem_addr(sm.kq[st][0]), 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t at = d + (i >> 2) * 1024 + (i & 3) * 2;
+                mma_ss(leads, tmem + TM_KK, at, at, idesc, i > 0);
             }
-            umma_commit(&sm.b_KK);
+            mma_commit(leads, &sm.b_KK);
         }
-        __syncwarp();
         const float beta = sm.beta[tp][t], dec = sm.dec[tp][t];
         float f = is_q ? f_own : f_own * beta;
         if (!strong) f *= sm.er[tp][t];
@@ -755,6 +804,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
 
 __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
+    const uint32_t leads = elect_lane();
     DcWalk w;
     dc_start(w);
     constexpr uint32_t i64 = idesc_f16(128, 64, false), i128 = idesc_f16(128, 128, true);
@@ -770,42 +820,42 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         dc_wait(A, sm, &sm.b_kq[st], (n / DC_KV) & 1);
         dc_wait(A, sm, &sm.b_S, n & 1);
         tc_fence_after();
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 16; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_KS);
+            mma_ts(leads, tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+        mma_commit(leads, &sm.b_KS);
         // U = T R: (R lo, T hi), (R hi, T lo), (R hi, T hi)
         dc_wait(A, sm, &sm.b_R, n & 1);
         tc_fence_after();
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 12; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
+            mma_ts(leads, tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
                    i > 0);
-        umma_commit(&sm.b_U);
+        mma_commit(leads, &sm.b_U);
         // Q S, in the shadow of what U goes through next, once the chunk before has read its own
         if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) & 1], ((n - 1) / 2) & 1);
         tc_fence_after();
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 16; ++i)
-            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_QS);
+            mma_ts(leads, tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+        mma_commit(leads, &sm.b_QS);
         // the state's increment: k as the right operand, tokens along K
         dc_wait(A, sm, &sm.b_W, n & 1);
         tc_fence_after();
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
-        umma_commit(&sm.b_D);
-        umma_commit(&sm.b_free[st]);
+            mma_ts(leads, tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
+        mma_commit(leads, &sm.b_D);
+        mma_commit(leads, &sm.b_free[st]);
         // P U: (U lo, P hi), (U hi, P lo), (U hi, P hi)
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 12; ++i)
-            mma_ts(tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
+            mma_ts(leads, tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
                    t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_PU);
+        mma_commit(leads, &sm.b_PU);
     }
     if (*(volatile int *)&sm.stop) {  // a wait was given up: let what is in flight end before tensor memory goes
-        umma_commit(&sm.b_end);
+        if (leads) umma_commit(&sm.b_end);
         mbar_wait_bounded(&sm.b_end, 0, DEFAULT_WAIT_CYCLES);
     }
 }
@@ -1055,7 +1105,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.taddr;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.taddr, 0);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(DC_REG_CHAIN));
         dc_chain<T>(A, sm, tmem);
@@ -1065,8 +1115,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_HELP));
         if (warp == 12) {
-            if ((threadIdx.x & 31) == 0) dc_issue(A, sm, tmem);
-            __syncwarp();
+            dc_issue(A, sm, tmem);
         } else if (warp == 13)
             dc_store<T>(A, sm);
         else if (warp == 14)
