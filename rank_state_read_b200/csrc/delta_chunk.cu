@@ -29,6 +29,8 @@
 // wide, are exact in fp16 after a row's power of two.  (fp16 pairs hold 22 bits where bf16
 // pairs hold 16 and bf16 triples 24 for half as many products again.)  y goes back to 16
 // bits: bf16 outputs take hi alone (2^-12), fp16 outputs the pair.
+#include <cuda.h>
+
 #include <cstddef>
 
 #include "device_util.cuh"
@@ -43,9 +45,10 @@ constexpr int DC_C = 64;        // tokens of a chunk
 constexpr int DC_VW = 128;      // value columns of a slice
 constexpr int DC_CHAIN = 256, DC_PREP = 128;
 constexpr int DC_THREADS = DC_CHAIN + DC_PREP + 128;
-// registers a thread after the split: 2 x 128 x 168 + 128 x 120 + 128 x 56 = 512 x 128
+// registers a thread after the split: 256 x 168 + 128 x 120 + 128 x 56 = 512 x 128
 constexpr int DC_REG_CHAIN = 168, DC_REG_PREP = 120, DC_REG_HELP = 56;
 constexpr int DC_KV = 3;        // stages of q and k; everything else has two
+constexpr int DC_MOST_POLLS = 50000;  // about a second
 constexpr float DC_STRONG = 100.f;  // exponents of a chunk's decays within which 2^(G_i - G_j) factors
 
 // tensor memory columns
@@ -55,6 +58,10 @@ constexpr uint32_t TM_PU = 192;  // P U (64)
 constexpr uint32_t TM_S = 256;   // S hi, lo (64 each); then U~ hi, lo (32 each)
 constexpr uint32_t TM_R = 384;   // R hi, lo (32 each); then U hi, lo
 constexpr uint32_t TM_KK = 448;  // [K; Q] K^T (64)
+
+struct DcMaps {
+    CUtensorMap q, k, v, y;
+};
 
 struct DcSmem {
     // 1024-byte aligned operand tiles, rows of 128 bytes, 128-byte swizzle
@@ -68,7 +75,7 @@ struct DcSmem {
     float beta[2][DC_C], dec[2][DC_C], rest[2][DC_C], er[2][DC_C], ec[2][DC_C], gh[2][DC_C], gl[2][DC_C];
     float col[DC_C];                  // factor of k_j in A and P
     float x[32][36];                  // products on the way to T
-    float mx[2][2][2][DC_VW];         // column maxima of the two chain halves
+    uint32_t mx[2][2][DC_VW];         // column maxima of the two chain halves, two upper halves of fp32
     float gC[2];                      // the whole chunk's decay
     int strong[2];
     uint64_t b_ld[DC_KV], b_free[DC_KV], b_kq[DC_KV], b_v[2], b_vfree[2], b_sc[2], b_tp[2], b_out[2];
@@ -105,30 +112,26 @@ __device__ __forceinline__ uint32_t elect_lane()
     return r;
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t leads, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leads)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t leads, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leads)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t leads, uint64_t *bar)
-{
-    if (leads) umma_commit(bar);
-    __syncwarp();
-}
-
+// N products along K, N / 4 runs of 4: run i takes the left operand at a + 8 (4 order[i] + step) and
+// the right one at b + off[i] + step * stride
 // 32 columns of the warp's 32 lanes; tmem_ld_wait before the values are used
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
 {
@@ -284,20 +287,32 @@ __device__ __forceinline__ void dc_next(const DeltaArgs &A, const DcSmem &sm, Dc
     dc_fetch(A, sm, w);
 }
 
-// ---- waits: bounded; past the plan's limit recorded, past the default limit given up, after
-// which nothing waits any more and the kernel runs out ----
+// ---- waits: a number of polls of up to 20 us each; past the plan's limit recorded, past the
+// default limit given up, after which nothing waits any more and the kernel runs out ----
+__device__ __forceinline__ bool dc_poll(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void dc_wait(const DeltaArgs &A, DcSmem &sm, uint64_t *bar, uint32_t parity)
 {
     if (mbar_test_wait(bar, parity)) return;
-    const long long t0 = clock64();
+    int left = A.polls;
     do {
-        const long long t = clock64() - t0;
-        if (t > A.wait_limit) {
+        if (--left < 0) {
             atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
-            if (t > DEFAULT_WAIT_CYCLES) *(volatile int *)&sm.stop = 1;
+            if (left < -DC_MOST_POLLS) *(volatile int *)&sm.stop = 1;
             if (*(volatile int *)&sm.stop) return;
         }
-    } while (!mbar_try_wait(bar, parity));
+    } while (!dc_poll(bar, parity));
 }
 
 // one arrival for a warp whose lanes have all done their part
@@ -307,105 +322,93 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// ---- warp 15: q, k, v of one chunk after the other, 16 bytes a lane ----
+// ---- q, k, v of one chunk after the other, by tensor copies of 64 rows.  Rows past the
+// sequence's end bring what lies there (or zeros): the readers leave them out ----
 
-// cp.async of 16 bytes, or 16 zero bytes
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool there)
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
 }
 
-// an arrival of this thread on `bar` once its copies so far have landed
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+__device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm, const DcMaps &maps)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// (A row of 128 or 256 bytes a bulk copy costs the copy engine some 60 cycles: 320 rows a chunk were
-// more than the chunk's products.)
-template <class T>
-__device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm)
-{
-    const int lane = threadIdx.x & 31, c = lane & 15, r0 = lane >> 4;  // 16 lanes a row, 2 rows a pass
-    DcWalk w;
-    dc_start(w);
-    for (int n = 0;; ++n) {
-        dc_next(A, sm, w);
-        if (!w.there) break;
-        const int st = n % DC_KV, sv = n & 1;
-        const long long t0 = w.first + w.chunk * DC_C;
-        const int left = w.len - w.chunk * DC_C;
-        const int hq = w.h / A.hpq;
-        if (n >= DC_KV) dc_wait(A, sm, &sm.b_free[st], (n / DC_KV - 1) & 1);
-        {
-            const T *k = static_cast<const T *>(A.k) + t0 * A.k_stride + hq * KDIM + c * 8;
-            const T *q = static_cast<const T *>(A.q) + t0 * A.q_stride + hq * KDIM + c * 8;
-            const uint32_t dst = smem_addr(sm.kq[st][c >> 3]);
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int t = 2 * i + r0;
-                const bool there = t < left;
-                const uint32_t at = dst + t * 128 + (((c ^ t) & 7) << 4);
-                cp_async16_zfill(at, there ? k + t * A.k_stride : k, there);
-                cp_async16_zfill(at + 64 * 128, there ? q + t * A.q_stride : q, there);
-            }
-            cp_async_arrive(&sm.b_ld[st]);
-        }
-        if (n >= 2) dc_wait(A, sm, &sm.b_vfree[sv], (n / 2 - 1) & 1);
-        {
-            const T *v = static_cast<const T *>(A.v) + t0 * A.v_stride + (long long)w.h * A.V + w.slice * DC_VW + c * 8;
-            if (w.slice * DC_VW + c * 8 < A.V) {
-#pragma unroll 4
-                for (int i = 0; i < 32; ++i) {
-                    const int t = 2 * i + r0;
-                    const bool there = t < left;
-                    cp_async16_zfill(smem_addr(&sm.v[sv][t][c * 8]), there ? v + t * A.v_stride : v, there);
+    const uint32_t leads = elect_lane();
+    DcWalk w, ahead;
+    dc_start(ahead);
+    // q and k go one chunk before v: they are needed earlier, and v's place is free later
+#pragma unroll 1
+    for (int n = -1;; ++n) {
+        w = ahead;
+        dc_next(A, sm, ahead);
+        if (ahead.there) {
+            const int st = (n + 1) % DC_KV;
+            if (n + 1 >= DC_KV) dc_wait(A, sm, &sm.b_free[st], ((n + 1) / DC_KV - 1) & 1);
+            if (leads) {
+                const int x = ahead.h / A.hpq * KDIM, y = ahead.first + ahead.chunk * DC_C;
+                const uint32_t dst = smem_addr(sm.kq[st][0]);
+                mbar_arrive_expect_tx(&sm.b_ld[st], 4 * 64 * 128);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    tma_load(dst + i * 128 * 128, &maps.k, x + 64 * i, y, &sm.b_ld[st]);
+                    tma_load(dst + i * 128 * 128 + 64 * 128, &maps.q, x + 64 * i, y, &sm.b_ld[st]);
                 }
             }
-            cp_async_arrive(&sm.b_v[sv]);
+            __syncwarp();
         }
+        if (n < 0) continue;
+        if (!w.there) break;
+        const int sv = n & 1;
+        if (n >= 2) dc_wait(A, sm, &sm.b_vfree[sv], (n / 2 - 1) & 1);
+        if (leads) {
+            mbar_arrive_expect_tx(&sm.b_v[sv], 64 * 256);
+            tma_load(smem_addr(sm.v[sv]), &maps.v, w.h * A.V + w.slice * DC_VW, w.first + w.chunk * DC_C, &sm.b_v[sv]);
+        }
+        __syncwarp();
     }
-    cp_async_commit();
-    cp_async_wait<0>();
 }
 
-// ---- warp 13: outputs, from the place of their chunk's values ----
+// ---- outputs, from the place of their chunk's values ----
 
 template <class T>
-__device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm)
+__device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm, const DcMaps &maps)
 {
     const int lane = threadIdx.x & 31, c = lane & 15, r0 = lane >> 4;
+    const uint32_t leads = elect_lane();
     DcWalk w;
     dc_start(w);
+#pragma unroll 1
     for (int n = 0;; ++n) {
         dc_next(A, sm, w);
         if (!w.there) break;
-        const int sv = n & 1;
-        const int left = w.len - w.chunk * DC_C;
-        T *y = static_cast<T *>(A.y) + (long long)(w.first + w.chunk * DC_C) * A.y_stride + (long long)w.h * A.V +
-               w.slice * DC_VW + c * 8;
+        const int sv = n & 1, t0 = w.first + w.chunk * DC_C;
+        const int left = w.len - w.chunk * DC_C, cols = A.V - w.slice * DC_VW;
         dc_wait(A, sm, &sm.b_out[sv], (n / 2) & 1);
-        if (w.slice * DC_VW + c * 8 < A.V) {
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int t = 2 * i + r0;
-                if (t < left)
-                    *reinterpret_cast<uint4 *>(y + t * A.y_stride) = *reinterpret_cast<const uint4 *>(&sm.v[sv][t][c * 8]);
+        if (left >= DC_C && cols >= DC_VW) {
+            if (leads) {
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&maps.y),
+                             "r"(w.h * A.V + w.slice * DC_VW), "r"(t0), "r"(smem_addr(sm.v[sv]))
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             }
+        } else if (c * 8 < cols) {
+            T *y = static_cast<T *>(A.y) + (long long)(t0 + r0) * A.y_stride + (long long)w.h * A.V + w.slice * DC_VW + c * 8;
+#pragma unroll 1
+            for (int t = r0; t < min(left, DC_C); t += 2, y += 2 * A.y_stride)
+                *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(&sm.v[sv][t][c * 8]);
         }
         warp_arrive(&sm.b_vfree[sv]);
     }
+    if (leads) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
 }
 
-// ---- warp 14: the decays of a chunk's tokens, two tokens a lane ----
+// ---- the decays of a chunk's tokens, two tokens a lane ----
 
-__device__ __forceinline__ float pow2_of(long long d)  // 2^(d / 2^40), to fp32 accuracy
-{
-    const int i = (int)(d >> 40);
-    const float f = (float)(int)((d >> 16) & 0xffffff) * 0x1p-24f;
-    // exponents below the normal range give 0, above it infinity
-    return i < -126 ? 0.f : i > 127 ? __int_as_float(0x7f800000) : ex2(f) * __int_as_float((i + 127) << 23);
-}
+__device__ __forceinline__ float pow2_of(long long d) { return ex2((float)d * 0x1p-40f); }  // 2^(d / 2^40)
 
 __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
 {
@@ -458,18 +461,19 @@ __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
         load();  // those of chunk n + 1, on their way while chunk n's are written down
         if (n < 0) continue;
         if (n >= 2) dc_wait(A, sm, &sm.b_tp[b], (n / 2 - 1) & 1);  // chunk n - 2 has been prepared
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
+            const long long Gi = i ? G[1] : G[0];
             const bool lost = bad & (0xffffffffu >> (31 - lane));  // from that token on
-            const float g = (float)G[i] * 0x1p-40f;
-            sm.beta[b][t] = be[i];
-            sm.dec[b][t] = lost ? __int_as_float(0x7fc00000) : pow2_of(G[i]);
-            sm.rest[b][t] = pow2_of(end - G[i]);
-            sm.er[b][t] = pow2_of(G[i] - mid);
-            sm.ec[b][t] = pow2_of(mid - G[i]);
+            const float g = (float)Gi * 0x1p-40f;
+            sm.beta[b][t] = i ? be[1] : be[0];
+            sm.dec[b][t] = lost ? __int_as_float(0x7fc00000) : pow2_of(Gi);
+            sm.rest[b][t] = pow2_of(end - Gi);
+            sm.er[b][t] = pow2_of(Gi - mid);
+            sm.ec[b][t] = pow2_of(mid - Gi);
             sm.gh[b][t] = g;
-            sm.gl[b][t] = (float)(G[i] - (long long)(g * 0x1p40f)) * 0x1p-40f;
+            sm.gl[b][t] = (float)(Gi - (long long)(g * 0x1p40f)) * 0x1p-40f;
         }
         if (lane == 0) {
             const float span = fmaxf((float)(top - mid), (float)(mid - end)) * 0x1p-40f;
@@ -479,7 +483,7 @@ __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
     }
 }
 
-// ---- warps 8-11 ----
+// ---- A, P, T of one chunk ahead ----
 
 __device__ __forceinline__ float tf32_round(float x)
 {
@@ -628,6 +632,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         dc_next(A, sm, w);
         if (!w.there) break;
         const int st = n % DC_KV, tp = n & 1;
+        const bool there = t < w.len - w.chunk * DC_C;
         dc_wait(A, sm, &sm.b_ld[st], (n / DC_KV) & 1);
 
         // this thread's row of k or q: its norm, and (bf16) fp16 values at a power of two of their
@@ -640,6 +645,11 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
             const int sw = (r & 7) << 4;
             float2 s2[4] = {two(0.f), two(0.f), two(0.f), two(0.f)};
             float m = 0.f, mul = 1.f;
+            if (!there) {  // a row past the sequence's end: whatever lies there counts as zeros
+#pragma unroll 1
+                for (int i = 0; i < 256; i += 16)
+                    *reinterpret_cast<uint4 *>(row + (i >> 7) * (128 * 128) + (i & 127)) = make_uint4(0, 0, 0, 0);
+            }
             if (CONVERT || A.normalize) {
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
@@ -699,23 +709,42 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         warp_arrive(&sm.b_kq[st]);
         if (wq == 0) {
             tc_fence_after();
-            constexpr uint32_t idesc = idesc_f16(128, 64, false);
-            const uint64_t d = sdesc_sw128(smem_addr(sm.kq[st][0]), 16, 1024);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t at = d + (i >> 2) * 1024 + (i & 3) * 2;
-                mma_ss(leads, tmem + TM_KK, at, at, idesc, i > 0);
+            if (leads) {
+                constexpr uint32_t idesc = idesc_f16(128, 64, false);
+                const uint64_t d = sdesc_sw128(smem_addr(sm.kq[st][0]), 16, 1024);
+#pragma unroll 4
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t at = d + (i >> 2) * 1024 + (i & 3) * 2;
+                    mma_ss(tmem + TM_KK, at, at, idesc, i > 0);
+                }
+                umma_commit(&sm.b_KK);
             }
-            mma_commit(leads, &sm.b_KK);
+            __syncwarp();
         }
         const float beta = sm.beta[tp][t], dec = sm.dec[tp][t];
         float f = is_q ? f_own : f_own * beta;
         if (!strong) f *= sm.er[tp][t];
         const int last = is_q ? t : t - 1;
-        // this row of A or P; rows below 32 have zeros right of column 32, which stay from the start
-        float2 x[32];
         dc_wait(A, sm, &sm.b_KK, n & 1);
         tc_fence_after();
+        if (strong) {
+            // the chunk forgets so much that the factors of its decays leave fp32's range: the
+            // decays themselves, in place
+            const float gh = sm.gh[tp][t], gl = sm.gl[tp][t];
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+                float x[16];
+                tmem_ld16n(kk + c, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] = c + e <= last ? x[e] * ex2((gh - sm.gh[tp][c + e]) + (gl - sm.gl[tp][c + e])) : 0.f;
+                tmem_st16(kk + c, reinterpret_cast<const uint32_t (&)[16]>(x));
+            }
+            tmem_st_wait();
+        }
+        // this row of A or P; rows below 32 have zeros right of column 32, which stay from the start
+        float2 x[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             if (c < 2 * half + 2) {
@@ -737,15 +766,6 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[8 * c + e] = two(0.f);
-            }
-        }
-        if (strong) {
-            // the chunk forgets so much that the factors of its decays leave fp32's range
-            const float gh = sm.gh[tp][t], gl = sm.gl[tp][t];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                if (2 * e <= last) x[e].x *= ex2((gh - sm.gh[tp][2 * e]) + (gl - sm.gl[tp][2 * e]));
-                if (2 * e + 1 <= last) x[e].y *= ex2((gh - sm.gh[tp][2 * e + 1]) + (gl - sm.gl[tp][2 * e + 1]));
             }
         }
         if (!is_q) {
@@ -800,7 +820,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
     }
 }
 
-// ---- warp 12 ----
+// ---- the chain's products ----
 
 __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
 {
@@ -820,39 +840,54 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         dc_wait(A, sm, &sm.b_kq[st], (n / DC_KV) & 1);
         dc_wait(A, sm, &sm.b_S, n & 1);
         tc_fence_after();
-#pragma unroll
+        if (leads) {
+#pragma unroll 4
         for (int i = 0; i < 16; ++i)
-            mma_ts(leads, tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        mma_commit(leads, &sm.b_KS);
+            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+        umma_commit(&sm.b_KS);
+        }
+        __syncwarp();
         // U = T R: (R lo, T hi), (R hi, T lo), (R hi, T hi)
         dc_wait(A, sm, &sm.b_R, n & 1);
         tc_fence_after();
-#pragma unroll
+        if (leads) {
+#pragma unroll 4
         for (int i = 0; i < 12; ++i)
-            mma_ts(leads, tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
+            mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
                    i > 0);
-        mma_commit(leads, &sm.b_U);
+        umma_commit(&sm.b_U);
+        }
+        __syncwarp();
         // Q S, in the shadow of what U goes through next, once the chunk before has read its own
         if (n >= 1) dc_wait(A, sm, &sm.b_out[(n - 1) & 1], ((n - 1) / 2) & 1);
         tc_fence_after();
-#pragma unroll
+        if (leads) {
+#pragma unroll 4
         for (int i = 0; i < 16; ++i)
-            mma_ts(leads, tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        mma_commit(leads, &sm.b_QS);
+            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+        umma_commit(&sm.b_QS);
+        }
+        __syncwarp();
         // the state's increment: k as the right operand, tokens along K
         dc_wait(A, sm, &sm.b_W, n & 1);
         tc_fence_after();
-#pragma unroll
+        if (leads) {
+#pragma unroll 4
         for (int i = 0; i < 8; ++i)
-            mma_ts(leads, tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
-        mma_commit(leads, &sm.b_D);
-        mma_commit(leads, &sm.b_free[st]);
+            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
+        umma_commit(&sm.b_D);
+        umma_commit(&sm.b_free[st]);
+        }
+        __syncwarp();
         // P U: (U lo, P hi), (U hi, P lo), (U hi, P hi)
-#pragma unroll
+        if (leads) {
+#pragma unroll 4
         for (int i = 0; i < 12; ++i)
-            mma_ts(leads, tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
+            mma_ts(tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
                    t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
-        mma_commit(leads, &sm.b_PU);
+        umma_commit(&sm.b_PU);
+        }
+        __syncwarp();
     }
     if (*(volatile int *)&sm.stop) {  // a wait was given up: let what is in flight end before tensor memory goes
         if (leads) umma_commit(&sm.b_end);
@@ -860,7 +895,7 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
     }
 }
 
-// ---- warps 0-7 ----
+// ---- the chain ----
 
 template <class T>
 __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_t tmem)
@@ -870,14 +905,15 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
     const int col = quad * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
     int flip = 0;  // which of the two exchange buffers comes next
-    // maxima over both halves of this lane's column
+    // maxima over both halves of this lane's column (upper halves: the exponents are what is needed)
     auto both = [&](float &a, float &b) {
-        sm.mx[flip][g][0][col] = a;
-        sm.mx[flip][g][1][col] = b;
+        uint32_t m = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+        sm.mx[flip][g][col] = m;
         named_sync(1 + quad, 64);
-        a = fmaxf(a, sm.mx[flip][g ^ 1][0][col]);
-        b = fmaxf(b, sm.mx[flip][g ^ 1][1][col]);
+        m = __vmaxu2(m, sm.mx[flip][g ^ 1][col]);
         flip ^= 1;
+        a = __uint_as_float(m << 16);
+        b = __uint_as_float(m & 0xffff0000u);
     };
     // 32 values (16 pairs) times mul: hi parts to 16 columns at `hi`, lo parts at `lo`
     auto put = [&](const float2 *x, float mul, uint32_t hi, uint32_t lo) {
@@ -964,6 +1000,7 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
                 yp[(4 * i + 2) * DC_VW] = (uint16_t)p1;
                 yp[(4 * i + 3) * DC_VW] = (uint16_t)(p1 >> 16);
             }
+            fence_async_smem();
             tc_fence_before();
             warp_arrive(&sm.b_out[tq]);
         }
@@ -992,10 +1029,15 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
                 x[2 * i + 1] = __ffma2_rn(__fmul2_rn(x[2 * i + 1], two(-sS)), fk.b, __fmul2_rn(fv.b, v1));
                 m = max3(max3(m, x[2 * i]), x[2 * i + 1]);
             }
-            if (!own) {  // columns past the value dimension: what lies there is nobody's
+            const int left = own ? w.len - w.chunk * DC_C - 32 * g : 0;
+            if (left < 32) {  // past the sequence's end or the value dimension: nobody's values
                 m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = two(0.f);
+                for (int i = 0; i < 16; ++i) {
+                    if (2 * i >= left) x[i].x = 0.f;
+                    if (2 * i + 1 >= left) x[i].y = 0.f;
+                    m = max3(m, x[i]);
+                }
             }
             both(m, unused);
             pow2_scale(m, mul, sR);
@@ -1068,7 +1110,7 @@ __device__ __forceinline__ void dc_order(const DeltaArgs &A, DcSmem &sm)
 }
 
 template <class T>
-__global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaArgs A)
+__global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaArgs A, const __grid_constant__ DcMaps maps)
 {
     extern __shared__ __align__(1024) unsigned char raw_smem[];
     DcSmem &sm = *reinterpret_cast<DcSmem *>(raw_smem);
@@ -1080,12 +1122,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     if (threadIdx.x == 0) {
         sm.stop = 0;
         for (int i = 0; i < DC_KV; ++i) {
-            mbar_init(&sm.b_ld[i], 32);
+            mbar_init(&sm.b_ld[i], 1);
             mbar_init(&sm.b_free[i], 1);
             mbar_init(&sm.b_kq[i], DC_PREP / 32);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.b_v[i], 32);
+            mbar_init(&sm.b_v[i], 1);
             mbar_init(&sm.b_vfree[i], 1);
             mbar_init(&sm.b_sc[i], 1);
             mbar_init(&sm.b_tp[i], DC_PREP / 32);
@@ -1105,38 +1147,72 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.taddr, 0);
-    if (warp < 8) {
+    constexpr uint32_t tmem = 0;  // all columns of the SM's tensor memory: they start at 0
+    constexpr int WP = DC_CHAIN / 32, WH = WP + DC_PREP / 32;  // first warps of the other groups
+    if (warp < WP) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(DC_REG_CHAIN));
         dc_chain<T>(A, sm, tmem);
-    } else if (warp < 12) {
+    } else if (warp < WH) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_PREP));
         dc_prep<T>(A, sm, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DC_REG_HELP));
-        if (warp == 12) {
+        if (warp == WH) {
             dc_issue(A, sm, tmem);
-        } else if (warp == 13)
-            dc_store<T>(A, sm);
-        else if (warp == 14)
+        } else if (warp == WH + 1)
+            dc_store<T>(A, sm, maps);
+        else if (warp == WH + 2)
             dc_scalars(A, sm);
         else
-            dc_bring<T>(A, sm);
+            dc_bring(A, sm, maps);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(sm.taddr, 512);
+}
+
+// a map of a token tensor's 64-row, `box`-column tiles
+bool dc_map(CUtensorMap *m, int dtype, const void *p, long long cols, long long tokens, long long stride, int box, bool swizzle)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (Encode) nullptr;
+        }
+        return (Encode)f;
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {(cuuint32_t)box, DC_C}, ones[2] = {1, 1};
+    return encode && encode(m, dtype == SKETCHSSM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                            const_cast<void *>(p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class T>
 cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
     const long long items = (long long)a.rows * a.H * ((a.V + DC_VW - 1) / DC_VW);
+    const long long qk = (long long)a.Hqk * KDIM, hv = (long long)a.H * a.V;
+    DcMaps maps;
+    if (!dc_map(&maps.q, a.dtype, a.q, qk, a.tokens, a.q_stride, 64, true) ||
+        !dc_map(&maps.k, a.dtype, a.k, qk, a.tokens, a.k_stride, 64, true) ||
+        !dc_map(&maps.v, a.dtype, a.v, hv, a.tokens, a.v_stride, DC_VW, false) ||
+        !dc_map(&maps.y, a.dtype, a.y, hv, a.tokens, a.y_stride, DC_VW, false))
+        return cudaErrorInvalidValue;
+    DeltaArgs A = a;
+    A.polls = (int)(a.wait_limit / 40000 < DC_MOST_POLLS ? a.wait_limit / 40000 : DC_MOST_POLLS);
     cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(DcSmem));
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<T><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(a);
+    delta_chunk_kernel<T><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(A, maps);
     return cudaGetLastError();
 }
 
