@@ -192,12 +192,43 @@ __device__ __forceinline__ void pow2_scale(float m, float &mul, float &inv)
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
-// hi and lo fp16 parts of two scaled values
+// hi and lo fp16 parts of two scaled values: four instructions, the differences in fp32 straight
+// from the halves
 __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
 {
-    const __half2 h = __float22half2_rn(v);
-    hi = h2_bits(h);
-    lo = h2_bits(__float22half2_rn(__ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), v)));
+    hi = h2_bits(__float22half2_rn(v));
+    float2 d;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tsub.rn.f32.f16 %0, l, %3;\n\tsub.rn.f32.f16 %1, u, %4;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(hi), "f"(v.x), "f"(v.y));
+    lo = h2_bits(__float22half2_rn(make_float2(-d.x, -d.y)));
+}
+
+// s + sum of the squares of two packed values
+__device__ __forceinline__ float add_squares(uint32_t v, float s, const __nv_bfloat16 *)
+{
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tfma.rn.f32.bf16 %0, l, l, %0;\n\tfma.rn.f32.bf16 %0, u, u, %0;\n\t}"
+        : "+f"(s)
+        : "r"(v));
+    return s;
+}
+__device__ __forceinline__ float add_squares(uint32_t v, float s, const __half *)
+{
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tfma.rn.f32.f16 %0, l, l, %0;\n\tfma.rn.f32.f16 %0, u, u, %0;\n\t}"
+        : "+f"(s)
+        : "r"(v));
+    return s;
+}
+
+// two packed bf16 values times a power of two, as fp16
+__device__ __forceinline__ uint32_t scale_to_half(uint32_t v, uint32_t mul)
+{
+    float2 d;
+    asm("{\n\t.reg .b16 l, u, m, n;\n\tmov.b32 {l, u}, %2;\n\tmov.b32 {n, m}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, l, m, 0f00000000;\n\tfma.rn.f32.bf16 %1, u, m, 0f00000000;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(v), "r"(mul));
+    return h2_bits(__float22half2_rn(d));
 }
 
 // max(m, |v.x|, |v.y|), m not negative
@@ -485,12 +516,9 @@ __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
 
 // ---- A, P, T of one chunk ahead ----
 
-__device__ __forceinline__ float tf32_round(float x)
-{
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return __uint_as_float(r);
-}
+// the part of x that tf32 holds (13 low mantissa bits cleared); the rest, x - tf32_part(x), is exact
+// in fp32 and loses what is below 2^-23 of x in tf32
+__device__ __forceinline__ float tf32_part(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], const float (&b)[2])
 {
@@ -503,18 +531,19 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], con
 // L[16 MT x 8 KT] B[8 KT x 8] as MT tiles of 16 rows x 8 columns, three tf32 products each (in
 // accumulators of their own, so that none waits for another): fp32 accuracy.  l(m, i, k): L at
 // row i + lane / 4, column k + lane % 4; b(k): B at row k + lane % 4, column lane / 4; LOWER: L is
-// lower triangular.
+// lower triangular; the first 8 `from` rows of B are zeros.
 template <int MT, int KT, bool LOWER = false, class FL, class FB>
-__device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
+__device__ __forceinline__ void mul_tri(float (&d)[MT][4], int from, FL l, FB b)
 {
     float d1[MT][4] = {}, d2[MT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < KT; ++ks) {
+        if (ks < from) continue;
         float bh[2], bl[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = b(8 * ks + 4 * e);
-            bh[e] = tf32_round(x);
+            bh[e] = tf32_part(x);
             bl[e] = x - bh[e];
         }
 #pragma unroll
@@ -524,7 +553,7 @@ __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float x = l(m, 16 * m + 8 * (e & 1), 8 * ks + 4 * (e >> 1));
-                ah[e] = tf32_round(x);
+                ah[e] = tf32_part(x);
                 al[e] = x - ah[e];
             }
             mma_tf32(d1[m], al, bh);
@@ -538,15 +567,14 @@ __device__ __forceinline__ void mul_tri(float (&d)[MT][4], FL l, FB b)
         for (int e = 0; e < 4; ++e) d[m][e] += d1[m][e] + d2[m][e];
 }
 
-// T = (I + A)^-1 in place, A strictly lower triangular (zeros elsewhere), by the four warps of
-// the group: the 16 x 16 blocks on the diagonal by substitution (a column a lane), then
-// T21 = -T22 A21 T11 for blocks of 16 and of 32.  Substitution in blocks is as stable as
-// substitution; the powers of A that a product form needs would not be.
-__device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], int r)
+// T = (I + A)^-1 in place, A strictly lower triangular (zeros elsewhere): the 16 x 16 blocks on the
+// diagonal by substitution (a column a lane, two blocks a warp: rows 32 half .. + 31), then
+// T21 = -T22 A21 T11 for blocks of 16 and of 32 by all four warps of the group.  Substitution in
+// blocks is as stable as substitution; the powers of A that a product form needs would not be.
+__device__ __forceinline__ void invert_blocks(float (&M)[64][68], int half)
 {
-    const int wq = r >> 5, lane = r & 31, g = lane >> 2, t = lane & 3;
-    {
-        const int o = 16 * wq, j = lane & 15;
+    const int lane = threadIdx.x & 31;
+    const int o = 32 * half + (lane & 16), j = lane & 15;
         const float *L = &M[o][o];
         float x[16];
         x[0] = j == 0 ? 1.f : 0.f;
@@ -565,23 +593,24 @@ __device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], i
             x[i] = s0 + s1;
         }
         __syncwarp();
-        if (lane < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) M[o + i][o + j] = x[i];
-        }
-    }
-    named_sync(5, DC_PREP);
+        for (int i = 0; i < 16; ++i) M[o + i][o + j] = x[i];
+}
+
+__device__ __forceinline__ void invert_merge(float (&M)[64][68], float (&X)[32][36], int r)
+{
+    const int wq = r >> 5, lane = r & 31, g = lane >> 2, t = lane & 3;
     {
         const int o = 32 * (wq >> 1), n0 = 8 * (wq & 1), xr = 16 * (wq >> 1);
         const float *L21 = &M[o + 16 + g][o + t], *L22 = &M[o + 16 + g][o + 16 + t], *T11 = &M[o + t][o + n0 + g];
         float d[1][4] = {};
-        mul_tri<1, 2>(d, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
+        mul_tri<1, 2>(d, wq & 1, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
         float *x = &X[xr][n0];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[(g + 8 * (e >> 1)) * 36 + 2 * t + (e & 1)] = d[0][e];
         __syncwarp();
         float f[1][4] = {};
-        mul_tri<1, 2>(f, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
+        mul_tri<1, 2>(f, 0, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
         named_sync(5, DC_PREP);  // A21 has been read
 #pragma unroll
         for (int e = 0; e < 4; ++e) M[o + 16 + g + 8 * (e >> 1)][o + n0 + 2 * t + (e & 1)] = -f[0][e];
@@ -591,7 +620,7 @@ __device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], i
         const int n0 = 8 * wq;
         const float *L21 = &M[32 + g][t], *L22 = &M[32 + g][32 + t], *T11 = &M[t][n0 + g];
         float d[2][4] = {};
-        mul_tri<2, 4>(d, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
+        mul_tri<2, 4>(d, wq, [&](int, int i, int k) { return L21[i * 68 + k]; }, [&](int k) { return T11[k * 68]; });
         float *x = &X[0][n0];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -599,7 +628,7 @@ __device__ __forceinline__ void invert(float (&M)[64][68], float (&X)[32][36], i
             for (int e = 0; e < 4; ++e) x[(16 * m + g + 8 * (e >> 1)) * 36 + 2 * t + (e & 1)] = d[m][e];
         __syncwarp();
         float f[2][4] = {};
-        mul_tri<2, 4, true>(f, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
+        mul_tri<2, 4, true>(f, 0, [&](int, int i, int k) { return L22[i * 68 + k]; }, [&](int k) { return x[(k + t) * 36 + g]; });
         named_sync(5, DC_PREP);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -615,6 +644,16 @@ __device__ __forceinline__ float max_of(uint4 v, const __nv_bfloat16 *)
     auto a = [](uint32_t w) { return __habs2(*reinterpret_cast<__nv_bfloat162 *>(&w)); };
     const __nv_bfloat162 m = __hmax2(__hmax2(a(v.x), a(v.y)), __hmax2(a(v.z), a(v.w)));
     return fmaxf(__low2float(m), __high2float(m));
+}
+
+// 8 scaled values as fp16 parts, 16 bytes each
+__device__ __forceinline__ void put8(uint8_t *hi, uint8_t *lo, const float2 *x, float mul)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(__fmul2_rn(x[e], two(mul)), h[e], l[e]);
+    *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 template <class T>
@@ -643,7 +682,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
             constexpr bool CONVERT = sizeof(T) == 2 && !__is_same(T, __half);
             uint8_t *row = sm.kq[st][0] + r * 128;
             const int sw = (r & 7) << 4;
-            float2 s2[4] = {two(0.f), two(0.f), two(0.f), two(0.f)};
+            float ss[4] = {};
             float m = 0.f, mul = 1.f;
             if (!there) {  // a row past the sequence's end: whatever lies there counts as zeros
 #pragma unroll 1
@@ -667,8 +706,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
                             const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float2 f = unpack2(v[e], (const T *)nullptr);
-                                s2[e] = __ffma2_rn(f, f, s2[e]);
+                                ss[e] = add_squares(v[e], ss[e], (const T *)nullptr);
                             }
                         }
                     }
@@ -688,15 +726,14 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[e] = h2_bits(__float22half2_rn(__fmul2_rn(unpack2(v[e], (const T *)nullptr), two(mul))));
+                            o[e] = scale_to_half(v[e], __float_as_uint(mul));
                         *reinterpret_cast<uint4 *>(row + hf * (128 * 128) + ((c << 4) ^ sw)) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
             }
             if (A.normalize) {
-                const float2 s = __fadd2_rn(__fadd2_rn(s2[0], s2[1]), __fadd2_rn(s2[2], s2[3]));
-                f_own *= rsqrtf(s.x + s.y + DELTA_QK_EPS);
+                f_own *= rsqrtf((ss[0] + ss[1]) + (ss[2] + ss[3]) + DELTA_QK_EPS);
             }
             if (is_q) f_own *= A.scale;
         }
@@ -774,49 +811,58 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
                 if (e < 8 * half + 8) st4(&sm.m[t][4 * e], make_float4(x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y));
         }
         named_sync(5, DC_PREP);
-        invert(sm.m, sm.x, r);
-        if (!is_q) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e < 8 * half + 8) {
-                    const Four v = lds_four(&sm.m[t][4 * e]);
-                    x[2 * e] = v.a;
-                    x[2 * e + 1] = v.b;
-                }
-        }
         // this stage of T, P and their factors is free once the chunk two before has given its outputs
         if (n >= 2) dc_wait(A, sm, &sm.b_out[tp], (n / 2 - 1) & 1);
-        {
+        const int sw = (t & 7) << 4;
+        if (is_q) {
             float m = 0.f, mul, inv;
 #pragma unroll
             for (int e = 0; e < 32; ++e) m = max3(m, x[e]);
             pow2_scale(m, mul, inv);
-            uint8_t *hi = sm.tp[tp][is_q ? 2 : 0] + t * 128, *lo = hi + 64 * 128;
-            const int sw = (t & 7) << 4;
+            uint8_t *hi = sm.tp[tp][2] + t * 128, *lo = hi + 64 * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (c < 4 * half + 4) {
-                    uint32_t h[4], l[4];
+            for (int c = 0; c < 8; ++c)
+                if (c < 4 * half + 4) put8(hi + ((c << 4) ^ sw), lo + ((c << 4) ^ sw), x + 4 * c, mul);
+            sm.fp[tp][t] = inv;
+            sm.fqs[tp][t] = dec * f_own;
+        } else {
+            invert_blocks(sm.m, half);
+            sm.fv[tp][t] = beta;
+            sm.fks[tp][t] = beta * dec * f_own;
+            sm.fw[tp][t] = sm.rest[tp][t] * f_own;
+            if (t == 63) sm.gC[tp] = dec;
+        }
+        named_sync(5, DC_PREP);
+        invert_merge(sm.m, sm.x, r);
+        {
+            // rows of T, two threads each: every other piece of 8 columns (left of column 32 in
+            // rows below it)
+            const int row = r >> 1;
+            float m = 0.f, mul, inv;
+            Four v[4][2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(__fmul2_rn(x[4 * c + e], two(mul)), h[e], l[e]);
-                    *reinterpret_cast<uint4 *>(hi + ((c << 4) ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(lo + ((c << 4) ^ sw)) = make_uint4(l[0], l[1], l[2], l[3]);
+            for (int i = 0; i < 4; ++i)
+                if (i < 2 || row >= 32) {
+                    v[i][0] = lds_four(&sm.m[row][16 * i + 8 * (r & 1)]);
+                    v[i][1] = lds_four(&sm.m[row][16 * i + 8 * (r & 1) + 4]);
+                    m = max3(max3(max3(max3(m, v[i][0].a), v[i][0].b), v[i][1].a), v[i][1].b);
                 }
-            }
-            if (is_q) {
-                sm.fp[tp][t] = inv;
-                sm.fqs[tp][t] = dec * f_own;
-            } else {
-                sm.fu[tp][t] = inv;
-                sm.fv[tp][t] = beta;
-                sm.fks[tp][t] = beta * dec * f_own;
-                sm.fw[tp][t] = sm.rest[tp][t] * f_own;
-                if (t == 63) sm.gC[tp] = dec;
-            }
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            pow2_scale(m, mul, inv);
+            uint8_t *hi = sm.tp[tp][0] + row * 128, *lo = hi + 64 * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < 2 || row >= 32) {
+                    const float2 y[4] = {v[i][0].a, v[i][0].b, v[i][1].a, v[i][1].b};
+                    const int at = ((2 * i + (r & 1)) << 4) ^ ((row & 7) << 4);
+                    put8(hi + at, lo + at, y, mul);
+                }
+            if (!(r & 1)) sm.fu[tp][row] = inv;
         }
         fence_async_smem();
         tc_fence_before();
         warp_arrive(&sm.b_tp[tp]);
+        named_sync(5, DC_PREP);  // T in fp32 has been read
     }
 }
 
