@@ -20,11 +20,12 @@
 #include "device_util.cuh"
 #include "dtype_util.cuh"
 #include "internal.cuh"
+#include "ptx_util.cuh"
 
 namespace sk {
 namespace {
 
-constexpr int DELTA_MAXT = 160;  // slabs of at most 80 columns
+constexpr int DELTA_MAXVS = 80;  // columns of a slab at most
 
 // Where a row's tokens lie and which state it has; false: nothing to do.  Every thread
 // of the CTA calls it.
@@ -52,141 +53,372 @@ __device__ __forceinline__ bool delta_row(const DeltaArgs &A, int row, long long
     return true;
 }
 
-// A token's rows as this thread needs them: 16 values of k and q, 4 of v, a, beta.
+// A token's rows as this thread needs them, as they came: 16 values of k and q, 4 of v, a, beta.
+template <class T, int KS>
 struct DeltaToken {
-    float4 k[4], q[4], v;
+    typename Raw4<T>::type k[32 / KS], q[32 / KS], v;
     float a, beta;
 };
 
-template <class T>
-__device__ __forceinline__ void delta_load(const DeltaArgs &A, long long t, int h, int hq, int ks, int col, DeltaToken &x)
+template <class T, int KS>
+__device__ __forceinline__ void delta_load(const DeltaArgs &A, long long t, int h, int hq, int ks, int col,
+                                           DeltaToken<T, KS> &x)
 {
     const T *k = static_cast<const T *>(A.k) + t * A.k_stride + hq * KDIM + 4 * ks;
     const T *q = static_cast<const T *>(A.q) + t * A.q_stride + hq * KDIM + 4 * ks;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x.k[i] = load4(k + 32 * i);
-        x.q[i] = load4(q + 32 * i);
+    for (int i = 0; i < 32 / KS; ++i) {
+        x.k[i] = load4_raw(k + 4 * KS * i);
+        x.q[i] = load4_raw(q + 4 * KS * i);
     }
-    x.v = load4(static_cast<const T *>(A.v) + t * A.v_stride + (long long)h * A.V + col);
+    x.v = load4_raw(static_cast<const T *>(A.v) + t * A.v_stride + (long long)h * A.V + col);
     x.a = __ldg(A.a + t * A.H + h);
     x.beta = __ldg(A.beta + t * A.H + h);
 }
 
-template <class T>
-__global__ void __launch_bounds__(DELTA_MAXT, 2) delta_kernel(const DeltaArgs A)
+// One token: y written (lanes with bit 0 of the row slice set and bit 3 clear), the state s moved
+// on.  KS row slices a column chunk (8, or 16 where lane bit 3 counts too): a thread holds
+// 128 / KS rows in quads 4 ks + 4 KS i.  y: this thread's 4 columns.
+template <class T, int KS>
+__device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken<T, KS> &c, float4 (&s)[128 / KS], T *y)
 {
+    constexpr int Q = 32 / KS;
+    constexpr unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, ks = lane & (KS - 1);
+    const float4 cv = values(c.v, (const T *)nullptr);
+    float kk = 0.f, qq = 0.f, qk = 0.f;
+    float4 d = zero4(), p = zero4();
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const float4 k4 = values(c.k[i], (const T *)nullptr), q4 = values(c.q[i], (const T *)nullptr);
+        kk += dot4(k4, k4);
+        qq += dot4(q4, q4);
+        qk += dot4(q4, k4);
+        fma4(d, k4.x, s[4 * i + 0]);
+        fma4(d, k4.y, s[4 * i + 1]);
+        fma4(d, k4.z, s[4 * i + 2]);
+        fma4(d, k4.w, s[4 * i + 3]);
+        fma4(p, q4.x, s[4 * i + 0]);
+        fma4(p, q4.y, s[4 * i + 1]);
+        fma4(p, q4.z, s[4 * i + 2]);
+        fma4(p, q4.w, s[4 * i + 3]);
+    }
+#pragma unroll
+    for (int o = 1; o < KS; o <<= 1) {
+        kk += __shfl_xor_sync(FULL, kk, o);
+        qq += __shfl_xor_sync(FULL, qq, o);
+        qk += __shfl_xor_sync(FULL, qk, o);
+    }
+    const float rk = A.normalize ? rsqrtf(kk + DELTA_QK_EPS) : 1.f;
+    const float rq = A.scale * (A.normalize ? rsqrtf(qq + DELTA_QK_EPS) : 1.f);
+    // lanes with bit 0 clear take k^T S, the others q^T S; then bits 1 and 2 pick the
+    // column: lane bits (b2 b1) end with column 2 b1 + b2 of the chunk
+    const bool b0 = ks & 1, b1 = ks & 2, b2 = ks & 4;
+    float4 m, o4;
+    m.x = b0 ? p.x : d.x;
+    m.y = b0 ? p.y : d.y;
+    m.z = b0 ? p.z : d.z;
+    m.w = b0 ? p.w : d.w;
+    o4.x = b0 ? d.x : p.x;
+    o4.y = b0 ? d.y : p.y;
+    o4.z = b0 ? d.z : p.z;
+    o4.w = b0 ? d.w : p.w;
+    m.x += __shfl_xor_sync(FULL, o4.x, 1);
+    m.y += __shfl_xor_sync(FULL, o4.y, 1);
+    m.z += __shfl_xor_sync(FULL, o4.z, 1);
+    m.w += __shfl_xor_sync(FULL, o4.w, 1);
+    float m0 = b1 ? m.z : m.x, m1 = b1 ? m.w : m.y;
+    m0 += __shfl_xor_sync(FULL, b1 ? m.x : m.z, 2);
+    m1 += __shfl_xor_sync(FULL, b1 ? m.y : m.w, 2);
+    float sum = b2 ? m1 : m0;
+    sum += __shfl_xor_sync(FULL, b2 ? m0 : m1, 4);
+    if (KS == 16) sum += __shfl_xor_sync(FULL, sum, 8);
+    // u of the lane's column (lanes with bit 0 set compute it of garbage and take it
+    // from their neighbour)
+    const float vc = b1 ? (b2 ? cv.w : cv.z) : (b2 ? cv.y : cv.x);
+    float u = c.beta * (vc - c.a * rk * sum);
+    u = __shfl_sync(FULL, u, lane & ~1);
+    if (b0 && ks < 8) store1(y + (b1 ? 2 : 0) + (b2 ? 1 : 0), rq * fmaf(c.a, sum, rk * qk * u));
+    const int base = lane & ~7;
+    float4 u4;
+    u4.x = rk * __shfl_sync(FULL, u, base);
+    u4.y = rk * __shfl_sync(FULL, u, base + 4);
+    u4.z = rk * __shfl_sync(FULL, u, base + 2);
+    u4.w = rk * __shfl_sync(FULL, u, base + 6);
+#pragma unroll
+    for (int i = 0; i < 4 * Q; ++i) {
+        const float4 k4 = values(c.k[i >> 2], (const T *)nullptr);
+        const float kv = (i & 3) == 0 ? k4.x : (i & 3) == 1 ? k4.y : (i & 3) == 2 ? k4.z : k4.w;
+        s[i].x = fmaf(kv, u4.x, c.a * s[i].x);
+        s[i].y = fmaf(kv, u4.y, c.a * s[i].y);
+        s[i].z = fmaf(kv, u4.z, c.a * s[i].z);
+        s[i].w = fmaf(kv, u4.w, c.a * s[i].w);
+    }
+}
+
+// this thread's part of a state: from (LOAD) or to memory
+template <int KS>
+__device__ __forceinline__ void load_state(const float *Sg, int V, float4 (&s)[128 / KS])
+{
+#pragma unroll
+    for (int i = 0; i < 128 / KS; ++i)
+        s[i] = *reinterpret_cast<const float4 *>(Sg + (long long)(4 * KS * (i >> 2) + (i & 3)) * V);
+}
+template <int KS>
+__device__ __forceinline__ void store_state(float *Sg, int V, const float4 (&s)[128 / KS])
+{
+#pragma unroll
+    for (int i = 0; i < 128 / KS; ++i) st4(Sg + (long long)(4 * KS * (i >> 2) + (i & 3)) * V, s[i]);
+}
+
+// Sequences: one CTA of 2 VS threads per (row, head, slab); the next token's rows are loaded before
+// this token's products.
+template <class T>
+__global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaArgs A)
+{
+    constexpr int KS = 8;
     const int nslab = A.V / A.VS;
     const long long item = blockIdx.x;
     const int slab = (int)(item % nslab);
     const int h = (int)(item / nslab % A.H), row = (int)(item / nslab / A.H);
     const int hq = h / A.hpq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ks = lane & 7, col = slab * A.VS + (warp * 4 + (lane >> 3)) * 4;
-    constexpr unsigned FULL = 0xffffffffu;
-
+    const int ks = lane & (KS - 1), col = slab * A.VS + (warp * 4 + lane / KS) * 4;
     long long first, slot;
     int len;
     if (!delta_row(A, row, first, len, slot)) return;
 
     float *Sg = A.S + ((slot * A.H + h) * KDIM + 4 * ks) * A.V + col;
-    float4 s[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        s[i] = *reinterpret_cast<const float4 *>(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V);
-    DeltaToken x;
-    delta_load<T>(A, first, h, hq, ks, col, x);
+    float4 s[128 / KS];
+    load_state<KS>(Sg, A.V, s);
+    DeltaToken<T, KS> x;
+    delta_load<T, KS>(A, first, h, hq, ks, col, x);
+    T *y = static_cast<T *>(A.y) + first * A.y_stride + (long long)h * A.V + col;
+    for (int t = 0; t < len; ++t, y += A.y_stride) {
+        const DeltaToken<T, KS> c = x;
+        if (t + 1 < len) delta_load<T, KS>(A, first + t + 1, h, hq, ks, col, x);
+        delta_token<T, KS>(A, c, s, y);
+    }
+    store_state<KS>(Sg, A.V, s);
+}
 
-    for (int t = 0; t < len; ++t) {
-        const DeltaToken c = x;
-        if (t + 1 < len) delta_load<T>(A, first + t + 1, h, hq, ks, col, x);
+// Single tokens of many rows: the states are all that counts, so the kernel is a stream of them.
+// Persistent CTAs of 8 warps, one per SM, take runs of neighbouring (row, head, slab) items; a
+// slab is a whole state up to 128 columns, one bulk copy, and three of them are on their way or
+// in use, so that some 128 KB a CTA are always in flight.  A warp has 16 rows of the slab, a lane
+// 4 columns of each: every access is a run of whole lines.  (The layout of the kernel above, 64
+// bytes of 8 rows a load, and loads into registers one item ahead stayed at 4.0 TB/s.)
+constexpr int DS_THREADS = 256, DS_STAGES = 3, DS_VW = 128;
 
-        float kk = 0.f, qq = 0.f, qk = 0.f;
-        float4 d = zero4(), p = zero4();
+struct DsSmem {
+    float part[2][8][2][DS_VW];  // the warps' shares of k^T S and q^T S
+    uint64_t full[DS_STAGES];
+    int slot[DS_STAGES], first[DS_STAGES];  // slot -1: a row to leave alone
+};
+
+// 16 values of a row that all lanes of a warp want
+template <class T>
+struct Row16 {
+    uint4 w[sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ void row16_load(const T *p, Row16<T> &x)
+{
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            kk += dot4(c.k[i], c.k[i]);
-            qq += dot4(c.q[i], c.q[i]);
-            qk += dot4(c.q[i], c.k[i]);
-            fma4(d, c.k[i].x, s[4 * i + 0]);
-            fma4(d, c.k[i].y, s[4 * i + 1]);
-            fma4(d, c.k[i].z, s[4 * i + 2]);
-            fma4(d, c.k[i].w, s[4 * i + 3]);
-            fma4(p, c.q[i].x, s[4 * i + 0]);
-            fma4(p, c.q[i].y, s[4 * i + 1]);
-            fma4(p, c.q[i].z, s[4 * i + 2]);
-            fma4(p, c.q[i].w, s[4 * i + 3]);
+    for (int i = 0; i < (int)sizeof(T); ++i) x.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+}
+__device__ __forceinline__ void row16_get(const Row16<float> &x, int i, float (&f)[4])  // values 4 i ..
+{
+    f[0] = __uint_as_float(x.w[i].x), f[1] = __uint_as_float(x.w[i].y), f[2] = __uint_as_float(x.w[i].z), f[3] = __uint_as_float(x.w[i].w);
+}
+template <class T>
+__device__ __forceinline__ void row16_get(const Row16<T> &x, int i, float (&f)[4])
+{
+    const uint4 w = x.w[i >> 1];
+    const float2 a = unpack2(i & 1 ? w.z : w.x, (const T *)nullptr), b = unpack2(i & 1 ? w.w : w.y, (const T *)nullptr);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+
+template <class T>
+__global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaArgs A, int VW, long long items)
+{
+    extern __shared__ __align__(128) unsigned char raw[];
+    DsSmem &sm = *reinterpret_cast<DsSmem *>(raw);
+    float *states = reinterpret_cast<float *>(raw + (sizeof(DsSmem) + 127) / 128 * 128);
+    const int nslab = A.V / VW, per = A.H * nslab;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = warp * 16;
+    const bool on = 4 * lane < VW;
+    const long long from = items * blockIdx.x / gridDim.x, to = items * (blockIdx.x + 1) / gridDim.x;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < DS_STAGES; ++i) mbar_init(&sm.full[i], 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+
+    // item i's state on its way to its stage (all threads: a new row's slot is checked together)
+    int row = -1;
+    long long first = 0, slot = 0;
+    bool good = false;
+    auto bring = [&](long long i) {
+        const int st = (int)((i - from) % DS_STAGES);
+        const int r = (int)(i / per), rest = (int)(i - (long long)r * per);
+        if (r != row) {
+            int len;
+            row = r;
+            good = delta_row(A, row, first, len, slot);
         }
+        if (warp == 0) {
+            if (lane == 0) {
+                sm.slot[st] = good ? (int)slot : -1;
+                sm.first[st] = (int)first;
+            }
+            if (good) {
+                const int h = rest / nslab;
+                const float *S = A.S + (slot * A.H + h) * KDIM * A.V + (rest - h * nslab) * VW;
+                float *dst = states + (size_t)st * KDIM * VW;
+                if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(KDIM * VW * 4));
+                __syncwarp();
+                if (nslab == 1) {
+                    if (lane == 0) bulk_copy_g2s(dst, S, (uint32_t)(KDIM * VW * 4), &sm.full[st]);
+                } else {
+                    for (int k = lane; k < KDIM; k += 32)
+                        bulk_copy_g2s(dst + k * VW, S + (long long)k * A.V, (uint32_t)(VW * 4), &sm.full[st]);
+                }
+            }
+        }
+    };
+    for (long long i = from; i < from + DS_STAGES && i < to; ++i) bring(i);
+    __syncthreads();
+
+    uint32_t phase = 0;  // parity of each stage's next copy
+    for (long long i = from; i < to; ++i) {
+        const int st = (int)((i - from) % DS_STAGES), pb = (int)((i - from) & 1);
+        const int h = (int)(i % per) / nslab, col = (int)(i % per % nslab) * VW + 4 * lane;
+        const int sl = sm.slot[st];
+        const long long tok = sm.first[st];
+        float4 s[16], v = zero4();
+        Row16<T> kr, qr;
+        float qk = 0.f, kk = 0.f, qq = 0.f, a = 0.f, beta = 0.f;
+        bool lost = false;
+        if (sl >= 0) {
+            const T *k = static_cast<const T *>(A.k) + tok * A.k_stride + h / A.hpq * KDIM;
+            const T *q = static_cast<const T *>(A.q) + tok * A.q_stride + h / A.hpq * KDIM;
+            row16_load(k + r0, kr);
+            row16_load(q + r0, qr);
+            const float4 k4 = values(load4_raw(k + 4 * lane), (const T *)nullptr);
+            const float4 q4 = values(load4_raw(q + 4 * lane), (const T *)nullptr);
+            if (on) v = values(load4_raw(static_cast<const T *>(A.v) + tok * A.v_stride + (long long)h * A.V + col), (const T *)nullptr);
+            a = __ldg(A.a + tok * A.H + h);
+            beta = __ldg(A.beta + tok * A.H + h);
+            kk = warp_sum(dot4(k4, k4));
+            qq = warp_sum(dot4(q4, q4));
+            qk = warp_sum(dot4(q4, k4));
+            if (!mbar_wait_bounded(&sm.full[st], phase >> st & 1, A.wait_limit)) {
+                atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
+                lost = !mbar_wait_bounded(&sm.full[st], phase >> st & 1, DEFAULT_WAIT_CYCLES);
+            }
+            phase ^= 1u << st;
+            const float *src = states + (size_t)st * KDIM * VW + r0 * VW + 4 * lane;
+            float4 d = zero4(), p = zero4();
+            if (on) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            kk += __shfl_xor_sync(FULL, kk, o);
-            qq += __shfl_xor_sync(FULL, qq, o);
-            qk += __shfl_xor_sync(FULL, qk, o);
-        }
-        const float rk = A.normalize ? rsqrtf(kk + DELTA_QK_EPS) : 1.f;
-        const float rq = A.scale * (A.normalize ? rsqrtf(qq + DELTA_QK_EPS) : 1.f);
-        // lanes with bit 0 clear take k^T S, the others q^T S; then bits 1 and 2 pick the
-        // column: lane bits (b2 b1) end with column 2 b1 + b2 of the chunk
-        const bool b0 = ks & 1, b1 = ks & 2, b2 = ks & 4;
-        float4 m, o4;
-        m.x = b0 ? p.x : d.x;
-        m.y = b0 ? p.y : d.y;
-        m.z = b0 ? p.z : d.z;
-        m.w = b0 ? p.w : d.w;
-        o4.x = b0 ? d.x : p.x;
-        o4.y = b0 ? d.y : p.y;
-        o4.z = b0 ? d.z : p.z;
-        o4.w = b0 ? d.w : p.w;
-        m.x += __shfl_xor_sync(FULL, o4.x, 1);
-        m.y += __shfl_xor_sync(FULL, o4.y, 1);
-        m.z += __shfl_xor_sync(FULL, o4.z, 1);
-        m.w += __shfl_xor_sync(FULL, o4.w, 1);
-        float m0 = b1 ? m.z : m.x, m1 = b1 ? m.w : m.y;
-        m0 += __shfl_xor_sync(FULL, b1 ? m.x : m.z, 2);
-        m1 += __shfl_xor_sync(FULL, b1 ? m.y : m.w, 2);
-        float sum = b2 ? m1 : m0;
-        sum += __shfl_xor_sync(FULL, b2 ? m0 : m1, 4);
-        // u of the lane's column (lanes with bit 0 set compute it of garbage and take it
-        // from their neighbour)
-        const float vc = b1 ? (b2 ? c.v.w : c.v.z) : (b2 ? c.v.y : c.v.x);
-        float u = c.beta * (vc - c.a * rk * sum);
-        u = __shfl_sync(FULL, u, lane & ~1);
-        if (b0) {
-            const float y = rq * fmaf(c.a, sum, rk * qk * u);
-            store1(static_cast<T *>(A.y) + (first + t) * A.y_stride + (long long)h * A.V + col + (b1 ? 2 : 0) + (b2 ? 1 : 0), y);
-        }
-        const int base = lane & ~7;
-        float4 u4;
-        u4.x = rk * __shfl_sync(FULL, u, base);
-        u4.y = rk * __shfl_sync(FULL, u, base + 4);
-        u4.z = rk * __shfl_sync(FULL, u, base + 2);
-        u4.w = rk * __shfl_sync(FULL, u, base + 6);
+                for (int j = 0; j < 4; ++j) {
+                    float kf[4], qf[4];
+                    row16_get(kr, j, kf);
+                    row16_get(qr, j, qf);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float4 k4 = c.k[i >> 2];
-            const float kv = (i & 3) == 0 ? k4.x : (i & 3) == 1 ? k4.y : (i & 3) == 2 ? k4.z : k4.w;
-            s[i].x = fmaf(kv, u4.x, c.a * s[i].x);
-            s[i].y = fmaf(kv, u4.y, c.a * s[i].y);
-            s[i].z = fmaf(kv, u4.z, c.a * s[i].z);
-            s[i].w = fmaf(kv, u4.w, c.a * s[i].w);
+                    for (int e = 0; e < 4; ++e) {
+                        s[4 * j + e] = lds4(src + (4 * j + e) * VW);
+                        fma4(d, kf[e], s[4 * j + e]);
+                        fma4(p, qf[e], s[4 * j + e]);
+                    }
+                }
+                st4(&sm.part[pb][warp][0][4 * lane], d);
+                st4(&sm.part[pb][warp][1][4 * lane], p);
+            }
+        }
+        if (__syncthreads_or(lost)) {
+            // given up: let the copies still on their way land (bounded) before the CTA exits
+            if (threadIdx.x == 0)
+                for (int j = 0; j < DS_STAGES; ++j) mbar_wait_bounded(&sm.full[j], phase >> j & 1, DEFAULT_WAIT_CYCLES);
+            __syncthreads();
+            return;
+        }
+        if (i + DS_STAGES < to) bring(i + DS_STAGES);
+        if (sl >= 0 && on) {
+            float4 d = zero4();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 x = lds4(&sm.part[pb][j][0][4 * lane]);
+                d.x += x.x, d.y += x.y, d.z += x.z, d.w += x.w;
+            }
+            const float rk = A.normalize ? rsqrtf(kk + DELTA_QK_EPS) : 1.f;
+            const float rq = A.scale * (A.normalize ? rsqrtf(qq + DELTA_QK_EPS) : 1.f);
+            const float ar = a * rk;
+            const float4 u = make_float4(beta * (v.x - ar * d.x), beta * (v.y - ar * d.y), beta * (v.z - ar * d.z),
+                                         beta * (v.w - ar * d.w));
+            float *Sg = A.S + (((long long)sl * A.H + h) * KDIM + r0) * A.V + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float kf[4];
+                row16_get(kr, j, kf);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float f = rk * kf[e];
+                    const float4 x = s[4 * j + e];
+                    st4(Sg + (long long)(4 * j + e) * A.V, make_float4(fmaf(f, u.x, a * x.x), fmaf(f, u.y, a * x.y),
+                                                                      fmaf(f, u.z, a * x.z), fmaf(f, u.w, a * x.w)));
+                }
+            }
+            if (warp == (int)(i & 7)) {
+                float4 p = zero4();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 x = lds4(&sm.part[pb][j][1][4 * lane]);
+                    p.x += x.x, p.y += x.y, p.z += x.z, p.w += x.w;
+                }
+                const float f = rk * qk;
+                store4(static_cast<T *>(A.y) + tok * A.y_stride + (long long)h * A.V + col,
+                       make_float4(rq * fmaf(a, p.x, f * u.x), rq * fmaf(a, p.y, f * u.y), rq * fmaf(a, p.z, f * u.z),
+                                   rq * fmaf(a, p.w, f * u.w)));
+            }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st4(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V, s[i]);
+}
+
+template <class T>
+cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
+{
+    const long long items = (long long)a.rows * a.H * (a.V / a.VS);
+    if (a.cu)
+        delta_kernel<T><<<(unsigned)items, 2 * a.VS, 0, stream>>>(a);
+    else {
+        // One token a row.  With at least two states an SM the stream of whole states; below, more
+        // and smaller CTAs reach the memory sooner (one row of 32 heads of 128: 4.3 against 5.5 us).
+        const int VW = a.V <= DS_VW ? a.V : a.V / 2;
+        const long long whole = (long long)a.rows * a.H * (a.V / VW);
+        if (whole < 2LL * sms) {
+            delta_kernel<T><<<(unsigned)items, 2 * a.VS, 0, stream>>>(a);
+        } else {
+            const size_t smem = (sizeof(DsSmem) + 127) / 128 * 128 + (size_t)DS_STAGES * KDIM * VW * 4;
+            cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            delta_step_kernel<T><<<(unsigned)sms, DS_THREADS, smem, stream>>>(a, VW, whole);
+        }
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t stream)
+cudaError_t launch_delta(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
     if (a.rows == 0) return cudaSuccess;
-    const unsigned items = (unsigned)((long long)a.rows * a.H * (a.V / a.VS));
     switch (a.dtype) {
-    case SKETCHSSM_BF16: delta_kernel<__nv_bfloat16><<<items, 2 * a.VS, 0, stream>>>(a); break;
-    case SKETCHSSM_F16: delta_kernel<__half><<<items, 2 * a.VS, 0, stream>>>(a); break;
-    default: delta_kernel<float><<<items, 2 * a.VS, 0, stream>>>(a); break;
+    case SKETCHSSM_BF16: return launch_type<__nv_bfloat16>(a, sms, stream);
+    case SKETCHSSM_F16: return launch_type<__half>(a, sms, stream);
+    default: return launch_type<float>(a, sms, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace sk

@@ -30,13 +30,29 @@ __device__ __forceinline__ unsigned pack2(float a, float b, const __half *)
     return *reinterpret_cast<const unsigned *>(&r);
 }
 
-// 4 values (read-only path; 16- or 8-byte aligned)
-__device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+// 4 values as they lie in memory (read-only path; 16- or 8-byte aligned), and as fp32
+template <class T>
+struct Raw4 {
+    typedef uint2 type;
+};
+template <>
+struct Raw4<float> {
+    typedef float4 type;
+};
+
+__device__ __forceinline__ float4 load4_raw(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 
 template <class T>
-__device__ __forceinline__ float4 load4(const T *p)
+__device__ __forceinline__ uint2 load4_raw(const T *p)
 {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+    return __ldg(reinterpret_cast<const uint2 *>(p));
+}
+
+__device__ __forceinline__ float4 values(float4 w, const float *) { return w; }
+
+template <class T>
+__device__ __forceinline__ float4 values(uint2 w, const T *p)
+{
     const float2 a = unpack2(w.x, p), b = unpack2(w.y, p);
     return make_float4(a.x, a.y, b.x, b.y);
 }
@@ -45,37 +61,56 @@ __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store1(__half *p, float x) { *p = __float2half_rn(x); }
 
-// 8 values (16-byte aligned; plain loads, so that an output may be its own input)
-__device__ __forceinline__ void load8(const float *p, float (&x)[8])
+__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+template <class T>
+__device__ __forceinline__ void store4(T *p, float4 x)
 {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(x.x, x.y, p), pack2(x.z, x.w, p));
 }
 
+// 8 values as they lie in memory (16-byte aligned; plain loads, so that an output may be its own
+// input), and as fp32
 template <class T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8])
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+
+template <class T>
+__device__ __forceinline__ void load8_raw(const T *p, Raw8<T> &x)
 {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const unsigned v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2(v[i], p);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+}
+
+__device__ __forceinline__ void values8(const Raw8<float> &r, float2 (&x)[4], const float *)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[2 * i] = make_float2(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+        x[2 * i + 1] = make_float2(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
     }
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&x)[8])
+template <class T>
+__device__ __forceinline__ void values8(const Raw8<T> &r, float2 (&x)[4], const T *p)
 {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    x[0] = unpack2(r.w[0].x, p);
+    x[1] = unpack2(r.w[0].y, p);
+    x[2] = unpack2(r.w[0].z, p);
+    x[3] = unpack2(r.w[0].w, p);
+}
+
+__device__ __forceinline__ void store8(float *p, const float2 (&x)[4])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
 
 template <class T>
-__device__ __forceinline__ void store8(T *p, const float (&x)[8])
+__device__ __forceinline__ void store8(T *p, const float2 (&x)[4])
 {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(pack2(x[0], x[1], p), pack2(x[2], x[3], p), pack2(x[4], x[5], p), pack2(x[6], x[7], p));
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(x[0].x, x[0].y, p), pack2(x[1].x, x[1].y, p), pack2(x[2].x, x[2].y, p),
+                                               pack2(x[3].x, x[3].y, p));
 }
 
 }  // namespace sk

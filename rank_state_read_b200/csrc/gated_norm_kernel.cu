@@ -7,8 +7,10 @@
 // One pass: a group's values stay in registers between the sum of squares and the store,
 // so the kernel moves x, z and out once and is bound by HBM.  A group belongs to LANES
 // lanes (8 to 32, the width / 8 vectors of 8 values dealt out round robin), so that short
-// groups share a warp; groups of more than 2048 values belong to a CTA.  Sums and
+// groups share a warp; groups of more than 512 values belong to a CTA.  Sums and
 // products are fp32; the only rounding to fewer bits is that of the stored value.
+#include <atomic>
+
 #include "device_util.cuh"
 #include "dtype_util.cuh"
 #include "internal.cuh"
@@ -17,78 +19,142 @@ namespace sk {
 namespace {
 
 constexpr int GN_THREADS = 256;
-constexpr int GN_WARP_MAX = 2048;  // widest group of one warp: 8 vectors a lane
 
-__device__ __forceinline__ float gn_act(float z, int sigmoid)
+// -inf becomes the lowest finite value, NaN stays
+__device__ __forceinline__ float gn_finite(float z)
 {
-    const float s = 1.f / (1.f + expf(-z));
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fFF7FFFFF;" : "=f"(r) : "f"(z));
+    return r;
+}
+
+// Gates of two values.  By the hardware's exponential and reciprocal (a few 2^-22) where the result is
+// rounded to 16 bits, by expf and a division for fp32; in pairs, since at 128 columns of bf16 the
+// instructions bound the kernel next to HBM (162 us for 32768 x 32 x 128 element by element).
+template <bool FAST>
+__device__ __forceinline__ float2 gn_gate(float2 z, bool sigmoid)
+{
+    float2 s;
+    if (FAST) {
+        const float2 e = __fmul2_rn(z, make_float2(-1.44269504f, -1.44269504f));
+        float2 x;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.x) : "f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.y) : "f"(e.y));
+        x = __fadd2_rn(x, make_float2(1.f, 1.f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(x.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(x.y));
+    } else {
+        s = make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
+    }
+    if (sigmoid) return s;
     // silu(-inf) = 0, not -inf * 0
-    return sigmoid ? s : (s == 0.f ? 0.f : z * s);
+    return __fmul2_rn(make_float2(gn_finite(z.x), gn_finite(z.y)), s);
 }
 
 // VECS vectors of 8 values a lane; LANES lanes (a power of two up to 32) or, with
-// LANES = GN_THREADS, the whole CTA hold one group.
+// LANES = 0, all of a CTA of as many warps as it takes hold one group.  The CTAs stay and go through the groups, the
+// next one's values on their way (as they are in memory) while one is worked on.
 template <class TX, class T, int VECS, int LANES>
 __global__ void __launch_bounds__(GN_THREADS) gated_norm_kernel(const NormArgs A)
 {
-    const long long item = ((long long)blockIdx.x * GN_THREADS + threadIdx.x) / LANES;
-    const int lane = threadIdx.x % LANES;
-    const bool there = item < A.items;
-    const long long row = there ? item / A.groups : 0;
-    const int group = there ? (int)(item - row * A.groups) : 0;
+    constexpr bool WHOLE = LANES == 0;
+    const int lanes = WHOLE ? blockDim.x : LANES, PER = WHOLE ? 1 : GN_THREADS / (WHOLE ? 1 : LANES);
+    const int lane = WHOLE ? threadIdx.x : threadIdx.x % (WHOLE ? 1 : LANES);
     const int nvec = A.width / 8;
-    const TX *x = static_cast<const TX *>(A.x) + row * A.x_stride + (long long)group * A.width;
-    const T *z = A.z ? static_cast<const T *>(A.z) + row * A.z_stride + (long long)group * A.width : nullptr;
-    const float *w = A.weight + (A.weight_groups > 1 ? (long long)group * A.width : 0);
-    T *out = static_cast<T *>(A.out) + row * A.out_stride + (long long)group * A.width;
-
-    float u[VECS][8], g[VECS][8];
-    float sum = 0.f;
+    const unsigned items = (unsigned)A.items, step = gridDim.x * PER;
+    Raw8<TX> xr[VECS];
+    Raw8<T> zr[VECS];
+    unsigned row = 0, group = 0;  // of the values in xr, zr
+    auto load = [&](unsigned item) {
+        if (item < items) {
+            row = item / (unsigned)A.groups;
+            group = item - row * (unsigned)A.groups;
+            const TX *x = static_cast<const TX *>(A.x) + row * A.x_stride + (long long)group * A.width;
+            const T *z = static_cast<const T *>(A.z) + row * A.z_stride + (long long)group * A.width;
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        const int v = lane + i * LANES;
-        if (there && v < nvec) {
-            load8(x + 8 * v, u[i]);
-            if (z) load8(z + 8 * v, g[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        const int v = lane + i * LANES;
-        if (there && v < nvec) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                g[i][e] = z ? gn_act(g[i][e], A.sigmoid) : 1.f;
-                if (A.gate_first) u[i][e] *= g[i][e];
-                sum = fmaf(u[i][e], u[i][e], sum);
+            for (int i = 0; i < VECS; ++i) {
+                const int v = lane + i * lanes;
+                if (v < nvec) {
+                    load8_raw(x + 8 * v, xr[i]);
+                    if (A.z) load8_raw(z + 8 * v, zr[i]);
+                }
             }
         }
-    }
-    if (LANES <= 32) {
+    };
+    unsigned item = blockIdx.x * PER + (WHOLE ? 0 : threadIdx.x / (WHOLE ? 1 : LANES));
+    load(item);
+    // (a CTA's threads leave the loop together: its first thread has its smallest item)
+    for (unsigned base = blockIdx.x * PER; base < items; base += step, item += step) {
+        const bool there = item < items;
+        float2 u[VECS][4], g[VECS][4];
+        T *out = static_cast<T *>(A.out) + row * A.out_stride + (long long)group * A.width;
+        const float *w = A.weight + (A.weight_groups > 1 ? (long long)group * A.width : 0);
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    } else {
-        __shared__ float part[GN_THREADS / 32];
-        sum = warp_sum(sum);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-        __syncthreads();
-        sum = 0.f;
+        for (int i = 0; i < VECS; ++i) {
+            values8(xr[i], u[i], (const TX *)nullptr);
+            values8(zr[i], g[i], (const T *)nullptr);
+        }
+        load(item + step);
+        float2 sum2 = make_float2(0.f, 0.f);
+        auto gates = [&](bool sigmoid) {
 #pragma unroll
-        for (int i = 0; i < GN_THREADS / 32; ++i) sum += part[i];
-    }
-    const float r = rsqrtf(sum / (float)A.width + A.eps);
+            for (int i = 0; i < VECS; ++i)
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        const int v = lane + i * LANES;
-        if (there && v < nvec) {
-            const float4 w0 = ldg4(w + 8 * v), w1 = ldg4(w + 8 * v + 4);
-            const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                for (int e = 0; e < 4; ++e) g[i][e] = gn_gate<sizeof(T) == 2>(g[i][e], sigmoid);
+        };
+        if (!A.z) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                u[i][e] *= r * ww[e];
-                if (!A.gate_first) u[i][e] *= g[i][e];
+            for (int i = 0; i < VECS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[i][e] = make_float2(1.f, 1.f);
+        } else if (A.sigmoid) {
+            gates(true);
+        } else {
+            gates(false);
+        }
+        if (A.gate_first) {
+#pragma unroll
+            for (int i = 0; i < VECS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    u[i][e] = __fmul2_rn(u[i][e], g[i][e]);
+                    g[i][e] = make_float2(1.f, 1.f);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+            if (there && lane + i * lanes < nvec) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum2 = __ffma2_rn(u[i][e], u[i][e], sum2);
             }
-            store8(out + 8 * v, u[i]);
+        float sum = sum2.x + sum2.y;
+        if (!WHOLE) {
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        } else {
+            __shared__ float part[2][GN_THREADS / 32];
+            float *p = part[(base - blockIdx.x * PER) / step & 1];
+            sum = warp_sum(sum);
+            if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = sum;
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < GN_THREADS / 32; ++i)
+                if (32 * i < lanes) sum += p[i];
+        }
+        const float r = rsqrtf(sum / (float)A.width + A.eps);
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int v = lane + i * lanes;
+            if (there && v < nvec) {
+                const float4 w0 = ldg4(w + 8 * v), w1 = ldg4(w + 8 * v + 4);
+                const float2 ww[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
+                                      make_float2(w1.z, w1.w)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[i][e] = __fmul2_rn(__fmul2_rn(u[i][e], __fmul2_rn(ww[e], make_float2(r, r))), g[i][e]);
+                store8(out + 8 * v, u[i]);
+            }
         }
     }
 }
@@ -96,8 +162,20 @@ __global__ void __launch_bounds__(GN_THREADS) gated_norm_kernel(const NormArgs A
 template <class TX, class T, int VECS, int LANES>
 cudaError_t launch_shape(const NormArgs &a, cudaStream_t stream)
 {
-    constexpr int PER = GN_THREADS / LANES;
-    gated_norm_kernel<TX, T, VECS, LANES><<<(unsigned)((a.items + PER - 1) / PER), GN_THREADS, 0, stream>>>(a);
+    const int warps = LANES ? GN_THREADS / 32 : (a.width / 8 + 32 * VECS - 1) / (32 * VECS);
+    const int per = LANES ? GN_THREADS / (LANES ? LANES : 1) : 1;
+    const long long blocks = (a.items + per - 1) / per;
+    // CTAs of each size that one SM holds, asked for once
+    static std::atomic<int> resident[GN_THREADS / 32 + 1];
+    int n = resident[warps].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gated_norm_kernel<TX, T, VECS, LANES>, 32 * warps, 0);
+        if (e != cudaSuccess) return e;
+        if (n < 1) n = 1;
+        resident[warps].store(n, std::memory_order_relaxed);
+    }
+    const long long most = (long long)n * a.sms;
+    gated_norm_kernel<TX, T, VECS, LANES><<<(unsigned)(blocks < most ? blocks : most), 32 * warps, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -109,10 +187,10 @@ cudaError_t launch_types(const NormArgs &a, cudaStream_t stream)
     if (nvec <= 16) return launch_shape<TX, T, 1, 16>(a, stream);
     if (nvec <= 32) return launch_shape<TX, T, 1, 32>(a, stream);
     if (nvec <= 64) return launch_shape<TX, T, 2, 32>(a, stream);
-    if (nvec <= 128) return launch_shape<TX, T, 4, 32>(a, stream);
-    if (a.width <= GN_WARP_MAX) return launch_shape<TX, T, 8, 32>(a, stream);
-    if (nvec <= 4 * GN_THREADS) return launch_shape<TX, T, 4, GN_THREADS>(a, stream);
-    return launch_shape<TX, T, 8, GN_THREADS>(a, stream);
+    if (nvec <= GN_THREADS) return launch_shape<TX, T, 1, 0>(a, stream);
+    if (nvec <= 2 * GN_THREADS) return launch_shape<TX, T, 2, 0>(a, stream);
+    if (nvec <= 4 * GN_THREADS) return launch_shape<TX, T, 4, 0>(a, stream);
+    return launch_shape<TX, T, 8, 0>(a, stream);
 }
 
 template <class TX>

@@ -134,7 +134,7 @@ struct DeltaArgs {
     long long wait_limit;
     int polls;  // the chunk kernel's wait limit in polls
 };
-cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t stream);
+cudaError_t launch_delta(const DeltaArgs &a, int sms, cudaStream_t stream);
 // prompts of 16-bit tokens, 64 at a time on the tensor cores
 constexpr int DC_MAX_SEQS = 512;
 bool delta_chunk_fits(const DeltaArgs &a);
@@ -144,7 +144,7 @@ cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream)
 constexpr int NORM_MAX_WIDTH = 16384;
 struct NormArgs {
     int x_dtype, dtype, groups, width, weight_groups;
-    int sigmoid, gate_first;
+    int sigmoid, gate_first, sms;
     float eps;
     long long items, x_stride, z_stride, out_stride;
     const void *x, *z;

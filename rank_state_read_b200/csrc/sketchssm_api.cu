@@ -398,7 +398,7 @@ sketchssm_status sketchssm_plan_check(const sketchssm_plan *p, sketchssm_stream 
     if (flags & sk::SK_STATUS_PREFILL_TIMEOUT)
         return fail(SKETCHSSM_ERR_TIMEOUT, "a prefill CTA waited past the plan's limit for its tensor-core products");
     if (flags & sk::SK_STATUS_DELTA_TIMEOUT)
-        return fail(SKETCHSSM_ERR_TIMEOUT, "a delta-rule CTA waited past the plan's limit for its tensor-core products");
+        return fail(SKETCHSSM_ERR_TIMEOUT, "a delta-rule CTA waited past the plan's limit for its copies or tensor-core products");
     return SKETCHSSM_OK;
 }
 
@@ -824,7 +824,7 @@ sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc 
     A.status = p->d_status;
     A.wait_limit = p->wait_limit;
     cudaError_t e = sk::delta_chunk_fits(A) ? sk::launch_delta_chunk(A, p->sms, (cudaStream_t)stream)
-                                            : sk::launch_delta(A, (cudaStream_t)stream);
+                                            : sk::launch_delta(A, p->sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule kernel launch");
     return SKETCHSSM_OK;
 }
@@ -883,6 +883,9 @@ extern "C" sketchssm_status sketchssm_gated_norm(const sketchssm_norm_desc *nd, 
     CHECK_T(z, zb, "z", true);
     CHECK_T(weight, fbytes(nd->weight_groups, nd->width), "weight", false);
     CHECK_T(out, ob, "out", false);
+    int dev = 0;
+    A.sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&A.sms, cudaDevAttrMultiProcessorCount, dev);
     A.x_dtype = nd->x_dtype;
     A.dtype = nd->dtype;
     A.groups = nd->groups;
