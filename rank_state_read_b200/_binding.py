@@ -104,8 +104,14 @@ def _check(status: int, where: str) -> None:
         raise SketchSSMError(status, where, load().sketchssm_last_error().decode())
 
 
+# the current stream's handle without the Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -161,6 +167,7 @@ class Plan:
         self.r_total = int(rt.value)
         self.offsets = list(off)
         self.rmax = list(rmax)
+        self._state_numel = batch * heads * key_dim * value_dim
         self.work = {}
         for n in range(1, window + 1):
             nw = ctypes.c_int32()
@@ -315,7 +322,10 @@ def sketchssm_flush_rows(plan: Plan, S, omega, kbuf, vbuf, abuf, bbuf, n_tokens,
 
 
 def _rows3(t, name: str, dtype, n: int, inner: int):
-    """Pointer and row stride of a tensor [n][x][y] whose rows are contiguous (x y = inner)."""
+    """Pointer and row stride (0: packed) of a tensor [n][x][y] whose rows are contiguous (x y = inner)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.dim() == 3
+            and t.numel() == n * inner and t.shape[0] == n and n):
+        return t.data_ptr(), 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -357,7 +367,7 @@ def _delta(plan: Plan, n: int, q, k, v, a, beta, S, y, normalize_qk, scale):
     vp, vs = _rows3(v, "v", dtype, n, hv)
     yp, ys = _rows3(y, "y", dtype, n, hv)
     td = TokenDesc(DTYPES[dtype], bool(normalize_qk), scale, qs, ks, vs, ys)
-    return td, (qp, kp, vp, _ptr(a, "a", n * H), _ptr(beta, "beta", n * H), _ptr(S, "S", plan.numel("S")), yp)
+    return td, (qp, kp, vp, _ptr(a, "a", n * H), _ptr(beta, "beta", n * H), _ptr(S, "S", plan._state_numel), yp)
 
 
 def sketchssm_delta_chunk(plan: Plan, cu, q, k, v, a, beta, S, y, *, slot=None, normalize_qk: bool = False,
