@@ -401,3 +401,142 @@ def test_nothing_to_do():
     torch.cuda.synchronize()
     c.plan.check()
     assert torch.equal(S, S0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,Hqk,V", [(4, 2, 128), (6, 2, 80), (4, 4, 256), (5, 1, 144), (4, 1, 16)])
+def test_step_of_many_rows(dtype, H, Hqk, V):
+    """Enough states that the step streams them (several a CTA): permuted slots, padding and a bad
+    slot among them, rows whose states one CTA starts and another ends."""
+    import torch
+    import rank_state_read_b200 as rs
+    rows = 151
+    slot = np.random.default_rng(20).permutation(rows + 2)[:rows].tolist()
+    slot[7] = slot[8] = slot[150] = -1
+    c = Case([1] * rows, rows + 2, H, Hqk, V, dtype, slot=slot, seed=20, unit=False)
+    c.slot_d[100] = rows + 2
+    rs.sketchssm_delta_step(c.plan, *c.args(), slot=c.slot_d, normalize_qk=True, scale=0.5)
+    with pytest.raises(rs.SketchSSMError):
+        c.plan.check()
+    c.slot[100] = -1
+    c.check(normalize=True, scale=0.5)
+    again = c.dev["S"].clone(), c.dev["y"].clone()
+    c2 = Case([1] * rows, rows + 2, H, Hqk, V, dtype, slot=slot, seed=20, unit=False)
+    c2.slot_d[100] = -1
+    rs.sketchssm_delta_step(c2.plan, *c2.args(), slot=c2.slot_d, normalize_qk=True, scale=0.5)
+    torch.cuda.synchronize()
+    c2.plan.check()
+    assert torch.equal(again[0], c2.dev["S"]) and torch.equal(again[1], c2.dev["y"])
+
+
+def test_step_equals_the_framework_s_own_step():
+    """fp32, packed, row i on state i: sketchssm_step computes the same."""
+    import torch
+    import rank_state_read_b200 as rs
+    for rows in (3, 160):
+        a, b = (Case([1] * rows, rows, 4, 2, 80, "float32", seed=21) for _ in range(2))
+        q, k, v, g, beta, S, y = a.args()
+        rs.sketchssm_delta_step(a.plan, q, k, v, g, beta, S, y)
+        rs.sketchssm_step(b.plan, *b.args())
+        torch.cuda.synchronize()
+        scale = float(b.dev["S"].abs().max())
+        assert float((a.dev["S"] - b.dev["S"]).abs().max()) <= 2 * state_tol(1) * scale * 12
+        assert float((a.dev["y"] - b.dev["y"]).abs().max()) <= 2 * state_tol(1) * scale * 12
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_many_sequences_of_mixed_lengths(dtype):
+    """More sequences than SMs, from nothing to many chunks, heads and slices dealt out over the CTAs
+    in several rounds; padding and a slot named twice among them."""
+    import torch
+    import rank_state_read_b200 as rs
+    g = np.random.default_rng(22)
+    lens = [int(x) for x in g.integers(0, 90, 60)] + [0, 300, 1, 64]
+    slot = g.permutation(len(lens)).tolist()
+    slot[5] = -1
+    c = Case(lens, len(lens), 5, 5, 144, dtype, slot=slot, seed=22)
+    twin = 40
+    assert lens[10] > 0 and lens[twin] > 0
+    c.slot_d[twin] = slot[10]
+    run_chunk(c)
+    with pytest.raises(rs.SketchSSMError):
+        c.plan.check()
+    c.slot[twin] = -1
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("chunk", [True, False])
+def test_short_wait_limit_is_reported_and_outputs_complete(dtype, chunk):
+    """With the plan's wait limit at one cycle the CTAs' waits run past it: recorded, and continued for
+    the same copies and products, so that the results are those of any other run."""
+    import torch
+    import rank_state_read_b200 as rs
+    rows = 3 if chunk else 160
+    lens = [130, 70, 64] if chunk else [1] * rows
+    a, b = (Case(lens, rows, 4, 2, 128, dtype, seed=23) for _ in range(2))
+    b.plan.set_wait_limit(1)
+    for c in (a, b):
+        if chunk:
+            run_chunk(c)
+        else:
+            rs.sketchssm_delta_step(c.plan, *c.args())
+    torch.cuda.synchronize()
+    assert torch.equal(a.dev["S"], b.dev["S"]) and torch.equal(a.dev["y"], b.dev["y"])
+    a.plan.check()
+    if chunk and dtype == "float32":
+        b.plan.check()  # token by token: nothing to wait for
+    else:
+        # the chain of a chunk certainly waits for its products; a step's copies may have landed
+        # before it looks for them, and then there is nothing to record
+        try:
+            b.plan.check()
+            assert not chunk
+        except rs.SketchSSMError as e:
+            assert e.status == 5
+    b.plan.set_wait_limit(2_000_000_000)
+    b.check()
+
+
+def test_two_streams_share_a_plan():
+    """Calls on one plan whose rows have different states may overlap: they share nothing but the
+    status word."""
+    import torch
+    import rank_state_read_b200 as rs
+    a = Case([130, 200], 4, 4, 2, 128, "bfloat16", slot=[0, 1], seed=24)
+    b = Case([90, 260], 4, 4, 2, 128, "bfloat16", slot=[2, 3], seed=24)
+    both = a.dev["S"]
+    b.dev["S"].copy_(both)
+    b.host["S"] = a.host["S"]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        both.copy_(b.dev["S"])
+        torch.cuda.synchronize()
+        for c, st in zip((a, b), streams):
+            q, k, v, g, beta, _, y = c.args()
+            rs.sketchssm_delta_chunk(a.plan, c.cu_d, q, k, v, g, beta, both, y, slot=c.slot_d, stream=st)
+        torch.cuda.synchronize()
+    a.plan.check()
+    for c in (a, b):
+        h = c.host
+        y, S, _ = delta_ref(c.cu, c.slot, h["q"], h["k"], h["v"], h["a"], h["beta"], h["S"])
+        top = np.sqrt((S * S).sum(2)).max()
+        got = both.double().cpu().numpy()[c.slot]
+        assert np.abs(got - S[c.slot]).max() <= state_tol(c.longest) * top
+        off = np.abs(c.dev["y"].double().cpu().numpy() - y) - c.eps * np.abs(y)
+        assert off.max() <= 2 * state_tol(c.longest) * top
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_strong_decays_next_to_weak_ones(dtype):
+    """Chunks whose decays span more than fp32's exponents beside chunks without decay: the products of
+    both are those of the definition, and nothing overflows on the way."""
+    def change(x):
+        g = np.random.default_rng(25)
+        x["a"][:64] = g.choice([1.0, 1e-8, 0.5], (64, x["a"].shape[1]))
+        x["a"][64:128] = 1.0
+        x["a"][128:192] = g.choice([1.0, 0.0], (64, x["a"].shape[1]), p=[0.9, 0.1])
+    c = Case([192 + 30], 1, 3, 1, 128, dtype, seed=25, change=change)
+    run_chunk(c)
+    c.check(grow=223 / 64)
