@@ -141,10 +141,12 @@ sketchssm_status sketchssm_plan_query(const sketchssm_plan *plan, int64_t *r_tot
 
 /*
  * Synchronise `stream`, then report what the kernels recorded on the plan since the
- * last check, and clear it: SKETCHSSM_ERR_TIMEOUT if a decode, flush, standard-step or
- * prefill CTA waited longer than the plan's wait limit (sketchssm_plan_set_wait_limit;
- * default about a second) for its own bulk copies (the Mamba-2 prefill: for its own
- * tensor-core products); SKETCHSSM_OK otherwise.  Such a CTA records the timeout and
+ * last check, and clear it: SKETCHSSM_ERR_TIMEOUT if a decode, flush, standard-step,
+ * prefill or delta-rule CTA waited longer than the plan's wait limit (sketchssm_plan_set_wait_limit;
+ * default about a second) for its own bulk copies (the Mamba-2 prefill and the chunked
+ * delta rule: for its own tensor-core products); SKETCHSSM_ERR_INVALID_ARG if a per-row
+ * position, token count, slot or range was out of range or a slot was named twice (those
+ * rows were left alone); SKETCHSSM_OK otherwise.  Such a CTA records the timeout and
  * keeps waiting, up to the default limit more, for the same operations, so the outputs
  * are complete unless that second wait also ran out (then the CTA gives up and its
  * outputs are incomplete).  No kernel waits on anything but its own operations, so a

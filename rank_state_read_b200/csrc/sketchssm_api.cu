@@ -752,7 +752,7 @@ sketchssm_status row_span(long long &stride, long long elems, long long rows, in
         return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is smaller than a row");
     if (stride * size % 16 != 0)
         return fail(SKETCHSSM_ERR_ALIGNMENT, std::string(name) + " stride is not a multiple of 16 bytes");
-    if (stride > (1LL << 40)) return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is too large");
+    if (stride > (1LL << 36)) return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is too large");
     *bytes = rows ? (size_t)((rows - 1) * stride + elems) * size : 0;
     return SKETCHSSM_OK;
 }

@@ -92,7 +92,7 @@ def test_chunk_lengths(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("H,Hqk,V", [(1, 1, 128), (6, 2, 80), (4, 1, 16), (3, 3, 144), (2, 1, 256), (5, 5, 96), (4, 2, 112)])
+@pytest.mark.parametrize("H,Hqk,V", [(1, 1, 128), (6, 2, 80), (4, 1, 16), (3, 3, 144), (2, 1, 256), (5, 5, 96), (4, 2, 112), (1, 1, 16)])
 def test_chunk_head_layouts(dtype, H, Hqk, V):
     c = Case([70, 0, 131], 3, H, Hqk, V, dtype, seed=2)
     run_chunk(c, scale=0.25)
