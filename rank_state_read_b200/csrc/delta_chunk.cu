@@ -13,22 +13,34 @@
 // so that the chain from chunk to chunk is three matrix products.  All exponents are
 // differences with j <= i, never positive; a decay of 0 counts as 2^-150.
 //
-// One CTA per (sequence, head, slice of 128 value columns), persistent.  Everything on the
-// chain is taken transposed: tensor-memory lane = value column.  A column's state (fp32)
-// lives in the registers of two threads, its 64 token values pass through them, and the
-// left operands S^T, R^T, U^T are written straight into tensor memory, with no shared
-// memory, no transposition and no sum across threads.
+// One CTA per (sequence, head, slice of 128 value columns), persistent, one per SM.  Everything
+// on the chain is taken transposed: tensor-memory lane = value column.  A column's state (fp32)
+// lives in the registers of two threads, its 64 token values pass through them, and the left
+// operands S^T, R^T, U^T are written straight into tensor memory, with no shared memory, no
+// transposition and no sum across threads.
 //   warps 0-7   the chain: warps w and w + 4 share 32 lanes (columns), each half the tokens
 //               (or key rows);
-//   warps 8-11  one chunk ahead: bring q, k, v in, and form A, P and T;
-//   warp 12     issues the chain's MMAs (its warp group gives its registers to the others).
+//   warps 8-11  one chunk ahead: q and k as operands, A, P and T;
+//   warp 12     issues the chain's MMAs;
+//   warp 13     writes the outputs, 14 forms the decays, 15 brings q, k and v (tensor copies).
 //
-// Precision.  The state is held, and its errors count, in fp32.  An operand x of the state's
-// path is split into two fp16 parts, x = 2^-e (hi + lo) (1 + 2^-22), e from the largest value
-// of its row, and products are taken hi hi + hi lo + lo hi in fp32; q and k, 8 or 11 bits
-// wide, are exact in fp16 after a row's power of two.  (fp16 pairs hold 22 bits where bf16
-// pairs hold 16 and bf16 triples 24 for half as many products again.)  y goes back to 16
-// bits: bf16 outputs take hi alone (2^-12), fp16 outputs the pair.
+// Precision.  The state is held, and its errors count, in fp32.  Every operand x but q and k is
+// split into two fp16 parts, x = 2^-e (hi + lo) (1 + 2^-22), e from the largest value of its row
+// (or column), and products are taken hi hi + hi lo + lo hi in fp32; q and k, 8 or 11 bits wide,
+// are exact in fp16 after a row's power of two.  (fp16 pairs hold 22 bits where bf16 pairs hold
+// 16, and bf16 triples hold 24 for half as many products again.)  y is rounded once.
+//
+// What bounds it.  The chain and the preparation each take some 9,700 SM cycles a chunk (of them
+// 2,560 of MMAs), and both wait for instructions more than for anything else: 2.5 of 6 stall
+// cycles an issued instruction.  A chunk runs some 60 KB of straight code, in 13 roles and
+// warps of their own, where straight code beyond 32 KB came at 5.7 cycles an instruction and SM in
+// a loop of nothing else.  Loops in its place (re-reading tensor memory, or the triangular
+// products in one loop) traded that for latency and were slower at one sequence.  One sequence of
+// 8192 tokens, 32 heads of 128, bf16: 642 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
+// 262 us; 48 of 32768: 937 us, 4.8 times what HBM needs for the bytes.  Token by token: 8369, 2058
+// and 7069 us.  Slower were: 16 chain warps with half the work each (1044 us for the one sequence),
+// T by a warp group of its own (758), rows of q, k and v by bulk copies of 128 and 256 bytes (the copy
+// engine takes some 60 cycles a copy).
 #include <cuda.h>
 
 #include <cstddef>

@@ -12,8 +12,7 @@
 // holds the float4 column chunk c4 of the 16 state rows 4 ks + 32 q + e in registers from
 // the first token to the last.  The sums over the 8 row slices of a column chunk are a
 // reduce-scatter over lane bits 0..2: 8 values (4 columns of k^T S and of q^T S) leave
-// one each in 8 lanes with 7 shuffles.  The next token's rows are loaded before this
-// token's products.  States are fp32 and every sum is taken in fp32.
+// one each in 8 lanes with 7 shuffles.  States are fp32 and every sum is taken in fp32.
 //
 // A row whose slot or bounds are bad, or whose slot an earlier row names too, is left
 // alone and reported through the plan's status word; a negative slot is padding.
@@ -54,42 +53,39 @@ __device__ __forceinline__ bool delta_row(const DeltaArgs &A, int row, long long
 }
 
 // A token's rows as this thread needs them, as they came: 16 values of k and q, 4 of v, a, beta.
-template <class T, int KS>
+template <class T>
 struct DeltaToken {
-    typename Raw4<T>::type k[32 / KS], q[32 / KS], v;
+    typename Raw4<T>::type k[4], q[4], v;
     float a, beta;
 };
 
-template <class T, int KS>
-__device__ __forceinline__ void delta_load(const DeltaArgs &A, long long t, int h, int hq, int ks, int col,
-                                           DeltaToken<T, KS> &x)
+template <class T>
+__device__ __forceinline__ void delta_load(const DeltaArgs &A, long long t, int h, int hq, int ks, int col, DeltaToken<T> &x)
 {
     const T *k = static_cast<const T *>(A.k) + t * A.k_stride + hq * KDIM + 4 * ks;
     const T *q = static_cast<const T *>(A.q) + t * A.q_stride + hq * KDIM + 4 * ks;
 #pragma unroll
-    for (int i = 0; i < 32 / KS; ++i) {
-        x.k[i] = load4_raw(k + 4 * KS * i);
-        x.q[i] = load4_raw(q + 4 * KS * i);
+    for (int i = 0; i < 4; ++i) {
+        x.k[i] = load4_raw(k + 32 * i);
+        x.q[i] = load4_raw(q + 32 * i);
     }
     x.v = load4_raw(static_cast<const T *>(A.v) + t * A.v_stride + (long long)h * A.V + col);
     x.a = __ldg(A.a + t * A.H + h);
     x.beta = __ldg(A.beta + t * A.H + h);
 }
 
-// One token: y written (lanes with bit 0 of the row slice set and bit 3 clear), the state s moved
-// on.  KS row slices a column chunk (8, or 16 where lane bit 3 counts too): a thread holds
-// 128 / KS rows in quads 4 ks + 4 KS i.  y: this thread's 4 columns.
-template <class T, int KS>
-__device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken<T, KS> &c, float4 (&s)[128 / KS], T *y)
+// One token: y written (by the lanes with bit 0 of the row slice set), the state s moved on.  y: this
+// thread's 4 columns.
+template <class T>
+__device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken<T> &c, float4 (&s)[16], T *y)
 {
-    constexpr int Q = 32 / KS;
     constexpr unsigned FULL = 0xffffffffu;
-    const int lane = threadIdx.x & 31, ks = lane & (KS - 1);
+    const int lane = threadIdx.x & 31, ks = lane & 7;
     const float4 cv = values(c.v, (const T *)nullptr);
     float kk = 0.f, qq = 0.f, qk = 0.f;
     float4 d = zero4(), p = zero4();
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float4 k4 = values(c.k[i], (const T *)nullptr), q4 = values(c.q[i], (const T *)nullptr);
         kk += dot4(k4, k4);
         qq += dot4(q4, q4);
@@ -104,7 +100,7 @@ __device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken
         fma4(p, q4.w, s[4 * i + 3]);
     }
 #pragma unroll
-    for (int o = 1; o < KS; o <<= 1) {
+    for (int o = 1; o < 8; o <<= 1) {
         kk += __shfl_xor_sync(FULL, kk, o);
         qq += __shfl_xor_sync(FULL, qq, o);
         qk += __shfl_xor_sync(FULL, qk, o);
@@ -132,13 +128,12 @@ __device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken
     m1 += __shfl_xor_sync(FULL, b1 ? m.y : m.w, 2);
     float sum = b2 ? m1 : m0;
     sum += __shfl_xor_sync(FULL, b2 ? m0 : m1, 4);
-    if (KS == 16) sum += __shfl_xor_sync(FULL, sum, 8);
     // u of the lane's column (lanes with bit 0 set compute it of garbage and take it
     // from their neighbour)
     const float vc = b1 ? (b2 ? cv.w : cv.z) : (b2 ? cv.y : cv.x);
     float u = c.beta * (vc - c.a * rk * sum);
     u = __shfl_sync(FULL, u, lane & ~1);
-    if (b0 && ks < 8) store1(y + (b1 ? 2 : 0) + (b2 ? 1 : 0), rq * fmaf(c.a, sum, rk * qk * u));
+    if (b0) store1(y + (b1 ? 2 : 0) + (b2 ? 1 : 0), rq * fmaf(c.a, sum, rk * qk * u));
     const int base = lane & ~7;
     float4 u4;
     u4.x = rk * __shfl_sync(FULL, u, base);
@@ -146,7 +141,7 @@ __device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken
     u4.z = rk * __shfl_sync(FULL, u, base + 2);
     u4.w = rk * __shfl_sync(FULL, u, base + 6);
 #pragma unroll
-    for (int i = 0; i < 4 * Q; ++i) {
+    for (int i = 0; i < 16; ++i) {
         const float4 k4 = values(c.k[i >> 2], (const T *)nullptr);
         const float kv = (i & 3) == 0 ? k4.x : (i & 3) == 1 ? k4.y : (i & 3) == 2 ? k4.z : k4.w;
         s[i].x = fmaf(kv, u4.x, c.a * s[i].x);
@@ -156,58 +151,49 @@ __device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken
     }
 }
 
-// this thread's part of a state: from (LOAD) or to memory
-template <int KS>
-__device__ __forceinline__ void load_state(const float *Sg, int V, float4 (&s)[128 / KS])
-{
-#pragma unroll
-    for (int i = 0; i < 128 / KS; ++i)
-        s[i] = *reinterpret_cast<const float4 *>(Sg + (long long)(4 * KS * (i >> 2) + (i & 3)) * V);
-}
-template <int KS>
-__device__ __forceinline__ void store_state(float *Sg, int V, const float4 (&s)[128 / KS])
-{
-#pragma unroll
-    for (int i = 0; i < 128 / KS; ++i) st4(Sg + (long long)(4 * KS * (i >> 2) + (i & 3)) * V, s[i]);
-}
-
-// Sequences: one CTA of 2 VS threads per (row, head, slab); the next token's rows are loaded before
-// this token's products.
+// Sequences, and single tokens of few rows: one CTA of 2 VS threads per (row, head, slab); the next
+// token's rows are loaded before this token's products.  A token costs a lone warp 0.56 us, which
+// its 450 instructions bound: tokens seven ahead in shared memory (0.68 us), two ahead in registers
+// or 8 state rows a thread (0.57 us), and pairs with the decays kept aside (0.64 us) took longer.
 template <class T>
 __global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaArgs A)
 {
-    constexpr int KS = 8;
     const int nslab = A.V / A.VS;
     const long long item = blockIdx.x;
     const int slab = (int)(item % nslab);
     const int h = (int)(item / nslab % A.H), row = (int)(item / nslab / A.H);
     const int hq = h / A.hpq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ks = lane & (KS - 1), col = slab * A.VS + (warp * 4 + lane / KS) * 4;
+    const int ks = lane & 7, col = slab * A.VS + (warp * 4 + (lane >> 3)) * 4;
     long long first, slot;
     int len;
     if (!delta_row(A, row, first, len, slot)) return;
 
     float *Sg = A.S + ((slot * A.H + h) * KDIM + 4 * ks) * A.V + col;
-    float4 s[128 / KS];
-    load_state<KS>(Sg, A.V, s);
-    DeltaToken<T, KS> x;
-    delta_load<T, KS>(A, first, h, hq, ks, col, x);
+    float4 s[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        s[i] = *reinterpret_cast<const float4 *>(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V);
+    DeltaToken<T> x;
+    delta_load<T>(A, first, h, hq, ks, col, x);
     T *y = static_cast<T *>(A.y) + first * A.y_stride + (long long)h * A.V + col;
     for (int t = 0; t < len; ++t, y += A.y_stride) {
-        const DeltaToken<T, KS> c = x;
-        if (t + 1 < len) delta_load<T, KS>(A, first + t + 1, h, hq, ks, col, x);
-        delta_token<T, KS>(A, c, s, y);
+        const DeltaToken<T> c = x;
+        if (t + 1 < len) delta_load<T>(A, first + t + 1, h, hq, ks, col, x);
+        delta_token<T>(A, c, s, y);
     }
-    store_state<KS>(Sg, A.V, s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st4(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V, s[i]);
 }
 
 // Single tokens of many rows: the states are all that counts, so the kernel is a stream of them.
-// Persistent CTAs of 8 warps, one per SM, take runs of neighbouring (row, head, slab) items; a
-// slab is a whole state up to 128 columns, one bulk copy, and three of them are on their way or
-// in use, so that some 128 KB a CTA are always in flight.  A warp has 16 rows of the slab, a lane
-// 4 columns of each: every access is a run of whole lines.  (The layout of the kernel above, 64
-// bytes of 8 rows a load, and loads into registers one item ahead stayed at 4.0 TB/s.)
+// Persistent CTAs of 8 warps, one per SM, take runs of neighbouring (row, head) items; a state of
+// up to 128 columns is one bulk copy, and three of them are on their way or in use, so that some
+// 128 KB a CTA are always in flight.  A warp has 16 rows of the state, a lane 4 columns of each:
+// every access is a run of whole lines.  512 rows of 32 heads of 128, bf16: 350 us,
+// 6.2 TB/s of states and tokens, 0.95 of the measured copy rate.  (The kernel
+// above takes 617 us for them, its layout with the next item's state loaded into registers 548 us; an
+// item index in 64 bits, whose divisions every thread waits for, cost 45 us.)
 constexpr int DS_THREADS = 256, DS_STAGES = 3, DS_VW = 128;
 
 struct DsSmem {
@@ -240,15 +226,16 @@ __device__ __forceinline__ void row16_get(const Row16<T> &x, int i, float (&f)[4
 }
 
 template <class T>
-__global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaArgs A, int VW, long long items)
+__global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaArgs A)
 {
     extern __shared__ __align__(128) unsigned char raw[];
     DsSmem &sm = *reinterpret_cast<DsSmem *>(raw);
     float *states = reinterpret_cast<float *>(raw + (sizeof(DsSmem) + 127) / 128 * 128);
-    const int nslab = A.V / VW, per = A.H * nslab;
+    const int V = A.V;
+    const int items = A.rows * A.H;  // the host has checked that it fits
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = warp * 16;
-    const bool on = 4 * lane < VW;
-    const long long from = items * blockIdx.x / gridDim.x, to = items * (blockIdx.x + 1) / gridDim.x;
+    const bool on = 4 * lane < V;
+    const int from = (int)((long long)items * blockIdx.x / gridDim.x), to = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
     if (threadIdx.x == 0) {
         for (int i = 0; i < DS_STAGES; ++i) mbar_init(&sm.full[i], 1);
         mbar_fence_init();
@@ -259,9 +246,9 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
     int row = -1;
     long long first = 0, slot = 0;
     bool good = false;
-    auto bring = [&](long long i) {
-        const int st = (int)((i - from) % DS_STAGES);
-        const int r = (int)(i / per), rest = (int)(i - (long long)r * per);
+    auto bring = [&](int i) {
+        const int st = (i - from) % DS_STAGES;
+        const int r = i / A.H, h = i - r * A.H;
         if (r != row) {
             int len;
             row = r;
@@ -271,29 +258,21 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
             if (lane == 0) {
                 sm.slot[st] = good ? (int)slot : -1;
                 sm.first[st] = (int)first;
+                if (good) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(KDIM * V * 4));
             }
-            if (good) {
-                const int h = rest / nslab;
-                const float *S = A.S + (slot * A.H + h) * KDIM * A.V + (rest - h * nslab) * VW;
-                float *dst = states + (size_t)st * KDIM * VW;
-                if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(KDIM * VW * 4));
-                __syncwarp();
-                if (nslab == 1) {
-                    if (lane == 0) bulk_copy_g2s(dst, S, (uint32_t)(KDIM * VW * 4), &sm.full[st]);
-                } else {
-                    for (int k = lane; k < KDIM; k += 32)
-                        bulk_copy_g2s(dst + k * VW, S + (long long)k * A.V, (uint32_t)(VW * 4), &sm.full[st]);
-                }
-            }
+            __syncwarp();
+            if (good && lane < KDIM / 8)  // 8 rows a copy: 4% faster than one copy
+                bulk_copy_g2s(states + (st * KDIM + 8 * lane) * V, A.S + ((slot * A.H + h) * KDIM + 8 * lane) * V,
+                              (uint32_t)(8 * V * 4), &sm.full[st]);
         }
     };
-    for (long long i = from; i < from + DS_STAGES && i < to; ++i) bring(i);
+    for (int i = from; i < from + DS_STAGES && i < to; ++i) bring(i);
     __syncthreads();
 
     uint32_t phase = 0;  // parity of each stage's next copy
-    for (long long i = from; i < to; ++i) {
-        const int st = (int)((i - from) % DS_STAGES), pb = (int)((i - from) & 1);
-        const int h = (int)(i % per) / nslab, col = (int)(i % per % nslab) * VW + 4 * lane;
+    for (int i = from; i < to; ++i) {
+        const int st = (i - from) % DS_STAGES, pb = (i - from) & 1;
+        const int h = i % A.H, col = 4 * lane;
         const int sl = sm.slot[st];
         const long long tok = sm.first[st];
         float4 s[16], v = zero4();
@@ -318,7 +297,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
                 lost = !mbar_wait_bounded(&sm.full[st], phase >> st & 1, DEFAULT_WAIT_CYCLES);
             }
             phase ^= 1u << st;
-            const float *src = states + (size_t)st * KDIM * VW + r0 * VW + 4 * lane;
+            const float *src = states + (size_t)st * KDIM * V + r0 * V + 4 * lane;
             float4 d = zero4(), p = zero4();
             if (on) {
 #pragma unroll
@@ -328,7 +307,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
                     row16_get(qr, j, qf);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[4 * j + e] = lds4(src + (4 * j + e) * VW);
+                        s[4 * j + e] = lds4(src + (4 * j + e) * V);
                         fma4(d, kf[e], s[4 * j + e]);
                         fma4(p, qf[e], s[4 * j + e]);
                     }
@@ -370,7 +349,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
                                                                       fmaf(f, u.z, a * x.z), fmaf(f, u.w, a * x.w)));
                 }
             }
-            if (warp == (int)(i & 7)) {
+            if (warp == (i & 7)) {
                 float4 p = zero4();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -389,22 +368,18 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
 template <class T>
 cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
-    const long long items = (long long)a.rows * a.H * (a.V / a.VS);
-    if (a.cu)
-        delta_kernel<T><<<(unsigned)items, 2 * a.VS, 0, stream>>>(a);
-    else {
-        // One token a row.  With at least two states an SM the stream of whole states; below, more
-        // and smaller CTAs reach the memory sooner (one row of 32 heads of 128: 4.3 against 5.5 us).
-        const int VW = a.V <= DS_VW ? a.V : a.V / 2;
-        const long long whole = (long long)a.rows * a.H * (a.V / VW);
-        if (whole < 2LL * sms) {
-            delta_kernel<T><<<(unsigned)items, 2 * a.VS, 0, stream>>>(a);
-        } else {
-            const size_t smem = (sizeof(DsSmem) + 127) / 128 * 128 + (size_t)DS_STAGES * KDIM * VW * 4;
-            cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            delta_step_kernel<T><<<(unsigned)sms, DS_THREADS, smem, stream>>>(a, VW, whole);
-        }
+    const long long states = (long long)a.rows * a.H;
+    // One token a row and states of up to 128 columns go through the stream of states, but for the
+    // fewest (32 heads of 128: one row 4.5 us by the first kernel, 4.9 by the stream; 2: 4.7, 4.9;
+    // 4: 7.0, 5.2; 128: 143, 94).  Wider states would be streamed by slabs, a copy for each of their
+    // rows: 320 states of 256 columns took 34 us that way, 28 by the first kernel.
+    if (a.cu || a.V > DS_VW || 2 * states <= sms) {
+        delta_kernel<T><<<(unsigned)(states * (a.V / a.VS)), 2 * a.VS, 0, stream>>>(a);
+    } else {
+        const size_t smem = (sizeof(DsSmem) + 127) / 128 * 128 + (size_t)DS_STAGES * KDIM * a.V * 4;
+        cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        delta_step_kernel<T><<<(unsigned)(states < sms ? states : sms), DS_THREADS, smem, stream>>>(a);
     }
     return cudaGetLastError();
 }
