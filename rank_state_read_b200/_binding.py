@@ -322,27 +322,27 @@ def sketchssm_flush_rows(plan: Plan, S, omega, kbuf, vbuf, abuf, bbuf, n_tokens,
         "sketchssm_flush_rows")
 
 
-def _rows3(t, name: str, dtype, n: int, inner: int):
-    """Pointer and row stride (0: packed) of a tensor [n][x][y] whose rows are contiguous (x y = inner)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.dim() == 3
-            and t.numel() == n * inner and t.shape[0] == n and n):
-        return t.data_ptr(), 0
+def _rows3(t, name: str, dtype, shape):
+    """Pointer and row stride (0: packed) of a tensor of this shape, [n][x][y], whose rows are contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return (t.data_ptr() if shape[0] else None), 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] * t.shape[2] != inner:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} rows of {inner} values in three dimensions")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, x, y = shape
     if n == 0:
         return None, 0
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and t.shape[2] != 1) or (s1 != t.shape[2] and t.shape[1] != 1):
+    if (s2 != 1 and y != 1) or (s1 != y and x != 1):
         raise ValueError(f"the rows of {name} must be contiguous")
     if n == 1:
         return t.data_ptr(), 0
-    if s0 < inner:
+    if s0 < x * y:
         raise ValueError(f"the rows of {name} overlap")
     return t.data_ptr(), s0
 
@@ -359,14 +359,15 @@ def _ints(t, name: str, numel: int):
 
 def _delta(plan: Plan, n: int, q, k, v, a, beta, S, y, normalize_qk, scale):
     d = plan.desc
-    H, qk, hv = d.heads, d.qk_heads * d.key_dim, d.heads * d.value_dim
+    H = d.heads
+    qk, hv = (n, d.qk_heads, d.key_dim), (n, H, d.value_dim)
     dtype = getattr(q, "dtype", None)
     if dtype not in DTYPES:
         raise TypeError(f"q must be a float32, bfloat16 or float16 tensor, got {dtype}")
-    qp, qs = _rows3(q, "q", dtype, n, qk)
-    kp, ks = _rows3(k, "k", dtype, n, qk)
-    vp, vs = _rows3(v, "v", dtype, n, hv)
-    yp, ys = _rows3(y, "y", dtype, n, hv)
+    qp, qs = _rows3(q, "q", dtype, qk)
+    kp, ks = _rows3(k, "k", dtype, qk)
+    vp, vs = _rows3(v, "v", dtype, hv)
+    yp, ys = _rows3(y, "y", dtype, hv)
     td = TokenDesc(DTYPES[dtype], bool(normalize_qk), scale, qs, ks, vs, ys)
     return td, (qp, kp, vp, _ptr(a, "a", n * H), _ptr(beta, "beta", n * H), _ptr(S, "S", plan._state_numel), yp)
 
@@ -413,10 +414,10 @@ def sketchssm_gated_norm(x, z, weight, out, *, eps: float = 1e-6, activation: st
         raise TypeError("out must be a float32, bfloat16 or float16 tensor")
     if activation not in GATES:
         raise ValueError(f"activation must be one of {sorted(GATES)}, got {activation!r}")
-    n, groups, width = x.shape
-    xp, xs = _rows3(x, "x", x.dtype, n, groups * width)
-    zp, zs = (None, 0) if z is None else _rows3(z, "z", out.dtype, n, groups * width)
-    op, os_ = _rows3(out, "out", out.dtype, n, groups * width)
+    n, groups, width = shape = x.shape
+    xp, xs = _rows3(x, "x", x.dtype, shape)
+    zp, zs = (None, 0) if z is None else _rows3(z, "z", out.dtype, shape)
+    op, os_ = _rows3(out, "out", out.dtype, shape)
     wg = 1 if isinstance(weight, torch.Tensor) and weight.numel() == width else groups
     nd = NormDesc(DTYPES[x.dtype], DTYPES[out.dtype], groups, width, wg, GATES[activation], bool(gate_first), eps,
                   xs, zs, os_)

@@ -327,6 +327,28 @@ def test_captured_calls_and_another_stream(dtype):
     c.check()
 
 
+@pytest.mark.parametrize("rows", [5, 160])
+def test_captured_steps(rows):
+    import torch
+    import rank_state_read_b200 as rs
+    c = Case([1] * rows, rows, 4, 2, 128, "bfloat16", slot=list(range(rows))[::-1], seed=26)
+    S0 = c.dev["S"].clone()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        rs.sketchssm_delta_step(c.plan, *c.args(), slot=c.slot_d)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rs.sketchssm_delta_step(c.plan, *c.args(), slot=c.slot_d)
+    c.dev["S"].copy_(S0)
+    c.slot_d[0] = -1  # a row that has left the batch since
+    c.slot[0] = -1
+    c.dev["y"].fill_(7)
+    g.replay()
+    c.check()
+    c.plan.check()
+
+
 def test_the_same_call_gives_the_same_bits():
     import torch
     out = []
