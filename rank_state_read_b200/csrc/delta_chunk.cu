@@ -32,8 +32,8 @@
 //
 // What bounds it.  The chain and the preparation each take some 9,700 SM cycles a chunk (of them
 // 2,560 of MMAs), and both wait for instructions more than for anything else: 2.5 of 6 stall
-// cycles an issued instruction.  A chunk runs some 60 KB of straight code, in 13 roles and
-// warps of their own, where straight code beyond 32 KB came at 5.7 cycles an instruction and SM in
+// cycles an issued instruction.  A chunk runs some 60 KB of straight code in six roles,
+// where straight code beyond 32 KB came at 5.7 cycles an instruction and SM in
 // a loop of nothing else.  Loops in its place (re-reading tensor memory, or the triangular
 // products in one loop) traded that for latency and were slower at one sequence.  One sequence of
 // 8192 tokens, 32 heads of 128, bf16: 642 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
