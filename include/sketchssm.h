@@ -366,6 +366,9 @@ typedef struct {
  *    whose bounds are not 0 <= cu[i] <= cu[i+1] <= tokens, is skipped, and
  *    sketchssm_plan_check reports SKETCHSSM_ERR_INVALID_ARG.
  *  - Sums and the state are fp32 (or exact splits of fp32); y is rounded once.
+ *  - A value that is infinite or no number reaches only its own sequence, in the heads that read
+ *    it: the state and the outputs from its token on, and maybe those of up to 63 tokens before
+ *    it, which are computed together with it.
  *  - seqs = 0 and tokens = 0 do nothing.  Nothing is allocated; the call can be captured
  *    into a graph.
  */

@@ -36,8 +36,8 @@
 // where straight code beyond 32 KB came at 5.7 cycles an instruction and SM in
 // a loop of nothing else.  Loops in its place (re-reading tensor memory, or the triangular
 // products in one loop) traded that for latency and were slower at one sequence.  One sequence of
-// 8192 tokens, 32 heads of 128, bf16: 642 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
-// 262 us; 48 of 32768: 937 us, 4.8 times what HBM needs for the bytes.  Token by token: 8369, 2058
+// 8192 tokens, 32 heads of 128, bf16: 645 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
+// 263 us; 48 of 32768: 940 us, 4.8 times what HBM needs for the bytes.  Token by token: 8369, 2058
 // and 7069 us.  Slower were: 16 chain warps with half the work each (1044 us for the one sequence),
 // T by a warp group of its own (758), rows of q, k and v by bulk copies of 128 and 256 bytes (the copy
 // engine takes some 60 cycles a copy).
@@ -142,8 +142,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
-// N products along K, N / 4 runs of 4: run i takes the left operand at a + 8 (4 order[i] + step) and
-// the right one at b + off[i] + step * stride
 // 32 columns of the warp's 32 lanes; tmem_ld_wait before the values are used
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
 {
@@ -303,7 +301,7 @@ __device__ __forceinline__ void dc_fetch(const DeltaArgs &A, const DcSmem &sm, D
         const int row = sm.order[k / per], rest = (int)(k % per);
         w.first = __ldg(A.cu + row);
         const int end = __ldg(A.cu + row + 1);
-        w.slot = A.slot ? __ldg(A.slot + row) : row;
+        w.slot = A.slot ? __ldg(A.slot + row) : A.before + row;
         if (w.first < 0 || end <= w.first || end > A.tokens || w.slot < 0 || w.slot >= A.slots ||
             (sm.dup[row >> 5] >> (row & 31) & 1))
             continue;
@@ -587,26 +585,26 @@ __device__ __forceinline__ void invert_blocks(float (&M)[64][68], int half)
 {
     const int lane = threadIdx.x & 31;
     const int o = 32 * half + (lane & 16), j = lane & 15;
-        const float *L = &M[o][o];
-        float x[16];
-        x[0] = j == 0 ? 1.f : 0.f;
+    const float *L = &M[o][o];
+    float x[16];
+    x[0] = j == 0 ? 1.f : 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) {
-            // the newest value last: it is the one to wait for
-            float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
+    for (int i = 1; i < 16; ++i) {
+        // the newest value last: it is the one to wait for
+        float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-            for (int k4 = 0; k4 < i; k4 += 4) {
-                const float4 a = lds4(L + i * 68 + k4);
-                s0 = fmaf(-a.x, x[k4], s0);
-                if (k4 + 1 < i) s1 = fmaf(-a.y, x[k4 + 1], s1);
-                if (k4 + 2 < i) s0 = fmaf(-a.z, x[k4 + 2], s0);
-                if (k4 + 3 < i) s1 = fmaf(-a.w, x[k4 + 3], s1);
-            }
-            x[i] = s0 + s1;
+        for (int k4 = 0; k4 < i; k4 += 4) {
+            const float4 a = lds4(L + i * 68 + k4);
+            s0 = fmaf(-a.x, x[k4], s0);
+            if (k4 + 1 < i) s1 = fmaf(-a.y, x[k4 + 1], s1);
+            if (k4 + 2 < i) s0 = fmaf(-a.z, x[k4 + 2], s0);
+            if (k4 + 3 < i) s1 = fmaf(-a.w, x[k4 + 3], s1);
         }
-        __syncwarp();
+        x[i] = s0 + s1;
+    }
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) M[o + i][o + j] = x[i];
+    for (int i = 0; i < 16; ++i) M[o + i][o + j] = x[i];
 }
 
 __device__ __forceinline__ void invert_merge(float (&M)[64][68], float (&X)[32][36], int r)
@@ -900,9 +898,9 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         tc_fence_after();
         if (leads) {
 #pragma unroll 4
-        for (int i = 0; i < 16; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_KS);
+            for (int i = 0; i < 16; ++i)
+                mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 8), k0 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+            umma_commit(&sm.b_KS);
         }
         __syncwarp();
         // U = T R: (R lo, T hi), (R hi, T lo), (R hi, T hi)
@@ -910,10 +908,10 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         tc_fence_after();
         if (leads) {
 #pragma unroll 4
-        for (int i = 0; i < 12; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
-                   i > 0);
-        umma_commit(&sm.b_U);
+            for (int i = 0; i < 12; ++i)
+                mma_ts(tmem + TM_A, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3), t0 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64,
+                       i > 0);
+            umma_commit(&sm.b_U);
         }
         __syncwarp();
         // Q S, in the shadow of what U goes through next, once the chunk before has read its own
@@ -921,9 +919,9 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         tc_fence_after();
         if (leads) {
 #pragma unroll 4
-        for (int i = 0; i < 16; ++i)
-            mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_QS);
+            for (int i = 0; i < 16; ++i)
+                mma_ts(tmem + TM_Q, tmem + TM_S + 8 * (i ^ 8), k0 + 512 + ((i >> 2) & 1) * 1024 + (i & 3) * 2, i64, i > 0);
+            umma_commit(&sm.b_QS);
         }
         __syncwarp();
         // the state's increment: k as the right operand, tokens along K
@@ -931,19 +929,19 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         tc_fence_after();
         if (leads) {
 #pragma unroll 4
-        for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
-        umma_commit(&sm.b_D);
-        umma_commit(&sm.b_free[st]);
+            for (int i = 0; i < 8; ++i)
+                mma_ts(tmem + TM_A, tmem + TM_S + 8 * (i ^ 4), kn + (i & 3) * 128, i128, i > 0);
+            umma_commit(&sm.b_D);
+            umma_commit(&sm.b_free[st]);
         }
         __syncwarp();
         // P U: (U lo, P hi), (U hi, P lo), (U hi, P hi)
         if (leads) {
 #pragma unroll 4
-        for (int i = 0; i < 12; ++i)
-            mma_ts(tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
-                   t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
-        umma_commit(&sm.b_PU);
+            for (int i = 0; i < 12; ++i)
+                mma_ts(tmem + TM_PU, tmem + TM_R + (i < 4 ? 32 : 0) + 8 * (i & 3),
+                       t0 + 1024 + ((i >> 2) == 1 ? 512 : 0) + (i & 3) * 2, i64, i > 0);
+            umma_commit(&sm.b_PU);
         }
         __syncwarp();
     }
@@ -1140,29 +1138,34 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
     }
 }
 
-// The order in which sequences are taken (longest first) and those whose slot an earlier one
-// names; block 0 reports bad ones.
+// A launch takes DC_MAX_SEQS sequences, which each CTA sorts by itself; 768 sequences of 64 tokens, 8
+// heads of 128: 452 us in two launches (token by token 1857 us).
+//
+// The order in which the launch's sequences are taken (longest first) and those whose slot an
+// earlier one names; block 0 reports bad ones.
 __device__ __forceinline__ void dc_order(const DeltaArgs &A, DcSmem &sm)
 {
     for (int i = threadIdx.x; i < (A.rows + 31) / 32; i += DC_THREADS) sm.dup[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < A.rows; i += DC_THREADS) {
-        const int c0 = __ldg(A.cu + i), c1 = __ldg(A.cu + i + 1), slot = A.slot ? __ldg(A.slot + i) : i;
-        const int len = c1 - c0;
+        const int c0 = __ldg(A.cu + i), c1 = __ldg(A.cu + i + 1), slot = A.slot ? __ldg(A.slot + i) : A.before + i;
+        const int len = (int)((unsigned)c1 - (unsigned)c0);  // (bad bounds may be any numbers)
         int rank = 0;
         bool dup = false;
         int d0 = __ldg(A.cu);
         for (int j = 0; j < A.rows; ++j) {
-            const int d1 = __ldg(A.cu + j + 1), other = d1 - d0;
+            const int d1 = __ldg(A.cu + j + 1), other = (int)((unsigned)d1 - (unsigned)d0);
             d0 = d1;
             rank += other > len || (other == len && j < i);
             if (A.slot && j < i) dup = dup || __ldg(A.slot + j) == slot;
         }
+        if (A.slot)
+            for (int j = -A.before; j < 0; ++j) dup = dup || __ldg(A.slot + j) == slot;
         dup = dup && slot >= 0;
         sm.order[rank] = (uint16_t)i;
         if (dup) atomicOr(&sm.dup[i >> 5], 1u << (i & 31));
         const bool bad = c0 < 0 || c1 < c0 || c1 > A.tokens;
-        if (blockIdx.x == 0 && (bad || (len > 0 && slot >= 0 && (dup || slot >= A.slots))))
+        if (blockIdx.x == 0 && slot >= 0 && (bad || (len > 0 && (dup || slot >= A.slots))))
             atomicOr(A.status, SK_STATUS_BAD_ROW);
     }
 }
@@ -1257,7 +1260,6 @@ bool dc_map(CUtensorMap *m, int dtype, const void *p, long long cols, long long 
 template <class T>
 cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
-    const long long items = (long long)a.rows * a.H * ((a.V + DC_VW - 1) / DC_VW);
     const long long qk = (long long)a.Hqk * KDIM, hv = (long long)a.H * a.V;
     DcMaps maps;
     if (!dc_map(&maps.q, a.dtype, a.q, qk, a.tokens, a.q_stride, 64, true) ||
@@ -1270,8 +1272,15 @@ cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(DcSmem));
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<T><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(A, maps);
-    return cudaGetLastError();
+    for (A.before = 0; A.before < a.rows; A.before += DC_MAX_SEQS) {
+        A.rows = a.rows - A.before < DC_MAX_SEQS ? a.rows - A.before : DC_MAX_SEQS;
+        A.cu = a.cu + A.before;
+        if (a.slot) A.slot = a.slot + A.before;
+        const long long items = (long long)A.rows * A.H * ((A.V + DC_VW - 1) / DC_VW);
+        delta_chunk_kernel<T><<<(unsigned)(items < sms ? items : sms), DC_THREADS, sizeof(DcSmem), stream>>>(A, maps);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -1281,7 +1290,7 @@ bool delta_chunk_fits(const DeltaArgs &a)
     // Sequences of up to 10 tokens on average go token by token: 32 heads of 128 columns, bf16, take
     // (tokens a sequence: token by token / here) 12: 10.0 / 14.2 us for one sequence, 44 / 43 for 16,
     // 641 / 568 for 256; 8: 7.9 / 14.0, 36 / 43, 510 / 569.
-    return a.cu && a.dtype != SKETCHSSM_F32 && a.rows <= DC_MAX_SEQS && a.tokens > 10LL * a.rows;
+    return a.cu && a.dtype != SKETCHSSM_F32 && a.tokens > 10LL * a.rows;
 }
 
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream)

@@ -132,11 +132,12 @@ struct DeltaArgs {
     void *y;
     int *status;
     long long wait_limit;
-    int polls;  // the chunk kernel's wait limit in polls
+    int polls;   // the chunk kernel's wait limit in polls
+    int before;  // its sequences that earlier launches of the call take (cu and slot point behind them)
 };
 cudaError_t launch_delta(const DeltaArgs &a, int sms, cudaStream_t stream);
 // prompts of 16-bit tokens, 64 at a time on the tensor cores
-constexpr int DC_MAX_SEQS = 512;
+constexpr int DC_MAX_SEQS = 512;  // of one launch
 bool delta_chunk_fits(const DeltaArgs &a);
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream);
 

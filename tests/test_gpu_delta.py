@@ -562,3 +562,74 @@ def test_strong_decays_next_to_weak_ones(dtype):
     c = Case([192 + 30], 1, 3, 1, 128, dtype, seed=25, change=change)
     run_chunk(c)
     c.check(grow=223 / 64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("slots", ["none", "turned"])
+def test_more_sequences_than_one_launch_takes(dtype, slots):
+    """Over a thousand sequences: in their own order without slots, and with slots turned round,
+    padding and one that a sequence of another launch has named."""
+    import rank_state_read_b200 as rs
+    g = np.random.default_rng(23)
+    lens = [int(x) for x in g.integers(0, 28, 1090)]
+    lens[3] = lens[514] = lens[1089] = 70
+    n = len(lens)
+    assert sum(lens) > 10 * n
+    slot = list(range(n)) if slots == "none" else list(range(n - 1, -1, -1))
+    if slots == "turned":
+        slot[20] = slot[700] = -1
+    c = Case(lens, n, 2, 1, 16, dtype, slot=slot, seed=23)
+    if slots == "none":
+        rs.sketchssm_delta_chunk(c.plan, c.cu_d, *c.args())
+        c.plan.check()
+    else:
+        c.slot_d[1089] = slot[3]
+        c.slot_d[1030] = slot[514]
+        assert lens[1030] > 0
+        run_chunk(c)
+        with pytest.raises(rs.SketchSSMError):
+            c.plan.check()
+        c.slot[1089] = c.slot[1030] = -1
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_padding_needs_no_bounds(dtype):
+    """A padded batch: the bounds behind the last sequence are whatever is there, the slots -1."""
+    import torch
+    c = Case([70, 40, 1, 1], 4, 2, 2, 128, dtype, slot=[2, 0, -1, -1], seed=24)
+    c.cu_d[3:] = torch.tensor([0, 1 << 30], dtype=torch.int32)
+    run_chunk(c)
+    c.plan.check()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_in_its_sequence(dtype, bad):
+    """Many sequences in each CTA, some with values that are not finite: the others give the bits
+    that they give without them."""
+    import torch
+    g = np.random.default_rng(25)
+    lens = [int(x) for x in g.integers(30, 150, 90)]
+    sick = list(range(1, 90, 4))
+    got = []
+    for spoil in (False, True):
+        c = Case(lens, 90, 5, 5, 144, dtype, seed=25)
+        if spoil:
+            for i in sick:
+                m = ("q", "k", "v", "a", "beta")[i // 4 % 5]
+                c.dev[m][c.cu[i] + lens[i] // 2] = bad
+            c.dev["S"][sick[0]] = bad
+        run_chunk(c)
+        c.plan.check()
+        got.append((c.dev["y"], c.dev["S"], c))
+    c = got[0][2]
+    well = [i for i in range(90) if i not in sick]
+    rows = torch.cat([torch.arange(c.cu[i], c.cu[i + 1]) for i in well]).cuda()
+    assert torch.equal(got[0][0][rows], got[1][0][rows])
+    assert torch.equal(got[0][1][well], got[1][1][well])
+    # and the outputs of whole chunks of 64 before the value are finite
+    for i in sick[1:]:
+        first = c.cu[i] + lens[i] // 2 // 64 * 64
+        assert bool(torch.isfinite(got[1][0][c.cu[i]:first].float()).all())
