@@ -37,8 +37,8 @@
 // a loop of nothing else.  Loops in its place (re-reading tensor memory, or the triangular
 // products in one loop) traded that for latency and were slower at one sequence.  One sequence of
 // 8192 tokens, 32 heads of 128, bf16: 645 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
-// 263 us; 48 of 32768: 940 us, 4.8 times what HBM needs for the bytes.  Token by token: 8369, 2058
-// and 7069 us.  Slower were: 16 chain warps with half the work each (1044 us for the one sequence),
+// 263 us; 48 of 32768: 940 us, 4.8 times what HBM needs for the bytes.  Token by token: 4705, 1193
+// and 4339 us.  Slower were: 16 chain warps with half the work each (1044 us for the one sequence),
 // T by a warp group of its own (758), rows of q, k and v by bulk copies of 128 and 256 bytes (the copy
 // engine takes some 60 cycles a copy).
 #include <cuda.h>
@@ -1287,10 +1287,11 @@ cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 
 bool delta_chunk_fits(const DeltaArgs &a)
 {
-    // Sequences of up to 10 tokens on average go token by token: 32 heads of 128 columns, bf16, take
-    // (tokens a sequence: token by token / here) 12: 10.0 / 14.2 us for one sequence, 44 / 43 for 16,
-    // 641 / 568 for 256; 8: 7.9 / 14.0, 36 / 43, 510 / 569.
-    return a.cu && a.dtype != SKETCHSSM_F32 && a.tokens > 10LL * a.rows;
+    // Sequences of up to 10 tokens on average, and a single one of up to 20, go token by token: 32
+    // heads of 128 columns, bf16, take (tokens a sequence: token by token / here) 10: 39 / 43 us for
+    // 16 sequences, 563 / 553 for 256; 12: 43 / 43, 625 / 552; one sequence 10: 8.8 / 13.9, 20: 13.5 / 14.1,
+    // 24: 15.1 / 14.1.
+    return a.cu && a.dtype != SKETCHSSM_F32 && a.tokens > (a.rows == 1 ? 20LL : 10LL * a.rows);
 }
 
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int sms, cudaStream_t stream)

@@ -16,6 +16,8 @@
 //
 // A row whose slot or bounds are bad, or whose slot an earlier row names too, is left
 // alone and reported through the plan's status word; a negative slot is padding.
+#include <climits>
+
 #include "device_util.cuh"
 #include "dtype_util.cuh"
 #include "internal.cuh"
@@ -25,6 +27,11 @@ namespace sk {
 namespace {
 
 constexpr int DELTA_MAXVS = 80;  // columns of a slab at most
+constexpr int DELTA_AHEAD = 4;   // tokens between a line's way into L2 and its use
+// Most sequences that are taken longest first: each CTA ranks them by itself.  (32 heads of 128,
+// in order / longest first: 24 of 1500 tokens 311 / 265 us, 64 of 1280 243 / 235, 64 of 6400
+// 982 / 907; 100 of 900 220 / 232.)
+constexpr int DELTA_SORT = 64;
 
 // Where a row's tokens lie and which state it has; false: nothing to do.  Every thread
 // of the CTA calls it.
@@ -52,6 +59,30 @@ __device__ __forceinline__ bool delta_row(const DeltaArgs &A, int row, long long
     return true;
 }
 
+// The sequence of rank `r` by length, longest first (up to DELTA_SORT of them).
+__device__ __forceinline__ int delta_ranked(const DeltaArgs &A, int r)
+{
+    __shared__ int4 len4[DELTA_SORT / 4];
+    __shared__ int found;
+    int *len = reinterpret_cast<int *>(len4);
+    for (int i = threadIdx.x; i < (A.rows + 3) / 4 * 4; i += blockDim.x)
+        len[i] = i < A.rows ? (int)((unsigned)__ldg(A.cu + i + 1) - (unsigned)__ldg(A.cu + i))  // (bad bounds may be any numbers)
+                            : INT_MIN;
+    __syncthreads();
+    for (int i = threadIdx.x; i < A.rows; i += blockDim.x) {
+        const int mine = len[i];
+        int rank = 0;
+        for (int j = 0; j < A.rows; j += 4) {
+            const int4 o = len4[j / 4];
+            rank += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
+                    (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
+        }
+        if (rank == r) found = i;
+    }
+    __syncthreads();
+    return found;
+}
+
 // A token's rows as this thread needs them, as they came: 16 values of k and q, 4 of v, a, beta.
 template <class T>
 struct DeltaToken {
@@ -74,31 +105,39 @@ __device__ __forceinline__ void delta_load(const DeltaArgs &A, long long t, int 
     x.beta = __ldg(A.beta + t * A.H + h);
 }
 
-// One token: y written (by the lanes with bit 0 of the row slice set), the state s moved on.  y: this
+// The pair i (rows 2 i, 2 i + 1) of this thread's 16 values of q or k.
+template <class T>
+__device__ __forceinline__ float2 pair_of(const typename Raw4<T>::type (&x)[4], int i)
+{
+    const float4 w = values(x[i >> 1], (const T *)nullptr);
+    return i & 1 ? make_float2(w.z, w.w) : make_float2(w.x, w.y);
+}
+
+// One token: y written (by the lanes with bit 0 of the row slice set), the state s moved on; s[i][c]: the
+// rows 2 i, 2 i + 1 of column c, so that packed products take pairs of k and q as they are.  y: this
 // thread's 4 columns.
 template <class T>
-__device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken<T> &c, float4 (&s)[16], T *y)
+__device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken<T> &c, float2 (&s)[8][4], T *y)
 {
     constexpr unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, ks = lane & 7;
     const float4 cv = values(c.v, (const T *)nullptr);
-    float kk = 0.f, qq = 0.f, qk = 0.f;
-    float4 d = zero4(), p = zero4();
+    float2 kk2 = make_float2(0.f, 0.f), qq2 = kk2, qk2 = kk2, d2[4] = {}, p2[4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 k4 = values(c.k[i], (const T *)nullptr), q4 = values(c.q[i], (const T *)nullptr);
-        kk += dot4(k4, k4);
-        qq += dot4(q4, q4);
-        qk += dot4(q4, k4);
-        fma4(d, k4.x, s[4 * i + 0]);
-        fma4(d, k4.y, s[4 * i + 1]);
-        fma4(d, k4.z, s[4 * i + 2]);
-        fma4(d, k4.w, s[4 * i + 3]);
-        fma4(p, q4.x, s[4 * i + 0]);
-        fma4(p, q4.y, s[4 * i + 1]);
-        fma4(p, q4.z, s[4 * i + 2]);
-        fma4(p, q4.w, s[4 * i + 3]);
+    for (int i = 0; i < 8; ++i) {
+        const float2 k = pair_of<T>(c.k, i), q = pair_of<T>(c.q, i);
+        kk2 = __ffma2_rn(k, k, kk2);
+        qq2 = __ffma2_rn(q, q, qq2);
+        qk2 = __ffma2_rn(q, k, qk2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            d2[e] = __ffma2_rn(k, s[i][e], d2[e]);
+            p2[e] = __ffma2_rn(q, s[i][e], p2[e]);
+        }
     }
+    float kk = kk2.x + kk2.y, qq = qq2.x + qq2.y, qk = qk2.x + qk2.y;
+    const float4 d = make_float4(d2[0].x + d2[0].y, d2[1].x + d2[1].y, d2[2].x + d2[2].y, d2[3].x + d2[3].y);
+    const float4 p = make_float4(p2[0].x + p2[0].y, p2[1].x + p2[1].y, p2[2].x + p2[2].y, p2[3].x + p2[3].y);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
         kk += __shfl_xor_sync(FULL, kk, o);
@@ -135,33 +174,33 @@ __device__ __forceinline__ void delta_token(const DeltaArgs &A, const DeltaToken
     u = __shfl_sync(FULL, u, lane & ~1);
     if (b0) store1(y + (b1 ? 2 : 0) + (b2 ? 1 : 0), rq * fmaf(c.a, sum, rk * qk * u));
     const int base = lane & ~7;
-    float4 u4;
-    u4.x = rk * __shfl_sync(FULL, u, base);
-    u4.y = rk * __shfl_sync(FULL, u, base + 4);
-    u4.z = rk * __shfl_sync(FULL, u, base + 2);
-    u4.w = rk * __shfl_sync(FULL, u, base + 6);
+    const int from[4] = {0, 4, 2, 6};
+    const float2 a2 = make_float2(c.a, c.a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float4 k4 = values(c.k[i >> 2], (const T *)nullptr);
-        const float kv = (i & 3) == 0 ? k4.x : (i & 3) == 1 ? k4.y : (i & 3) == 2 ? k4.z : k4.w;
-        s[i].x = fmaf(kv, u4.x, c.a * s[i].x);
-        s[i].y = fmaf(kv, u4.y, c.a * s[i].y);
-        s[i].z = fmaf(kv, u4.z, c.a * s[i].z);
-        s[i].w = fmaf(kv, u4.w, c.a * s[i].w);
+    for (int e = 0; e < 4; ++e) {
+        const float ue = rk * __shfl_sync(FULL, u, base + from[e]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[i][e] = __ffma2_rn(pair_of<T>(c.k, i), make_float2(ue, ue), __fmul2_rn(a2, s[i][e]));
     }
 }
 
 // Sequences, and single tokens of few rows: one CTA of 2 VS threads per (row, head, slab); the next
-// token's rows are loaded before this token's products.  A token costs a lone warp 0.56 us, which
-// its 450 instructions bound: tokens seven ahead in shared memory (0.68 us), two ahead in registers
-// or 8 state rows a thread (0.57 us), and pairs with the decays kept aside (0.64 us) took longer.
+// token's rows are loaded before this token's products, and the lines of tokens further ahead are
+// brought into L2.  32 heads of 128, fp32: one prompt of 500 tokens 214 us, 0.43 us a token, which its
+// 370 instructions and their latencies bound; 24 prompts of 1500 tokens in all 265 us.  Without the
+// lines brought ahead 282 and 315 us; in the order that the prompts come in 311 for the 24; with a
+// column's rows one by one 282 and 334.  Tokens seven ahead in shared memory, two ahead in
+// registers, two a turn of the loop, or 8 state rows a thread were slower.
 template <class T>
 __global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaArgs A)
 {
     const int nslab = A.V / A.VS;
     const long long item = blockIdx.x;
     const int slab = (int)(item % nslab);
-    const int h = (int)(item / nslab % A.H), row = (int)(item / nslab / A.H);
+    const int h = (int)(item / nslab % A.H);
+    int row = (int)(item / nslab / A.H);
+    if (A.sort) row = delta_ranked(A, row);
     const int hq = h / A.hpq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ks = lane & 7, col = slab * A.VS + (warp * 4 + (lane >> 3)) * 4;
@@ -170,20 +209,46 @@ __global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaAr
     if (!delta_row(A, row, first, len, slot)) return;
 
     float *Sg = A.S + ((slot * A.H + h) * KDIM + 4 * ks) * A.V + col;
-    float4 s[16];
+    float2 s[8][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        s[i] = *reinterpret_cast<const float4 *>(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V);
+    for (int i = 0; i < 8; ++i) {
+        const float *r = Sg + (long long)(32 * (i >> 1) + 2 * (i & 1)) * A.V;
+        const float4 x = *reinterpret_cast<const float4 *>(r), z = *reinterpret_cast<const float4 *>(r + A.V);
+        s[i][0] = make_float2(x.x, z.x);
+        s[i][1] = make_float2(x.y, z.y);
+        s[i][2] = make_float2(x.z, z.z);
+        s[i][3] = make_float2(x.w, z.w);
+    }
     DeltaToken<T> x;
     delta_load<T>(A, first, h, hq, ks, col, x);
     T *y = static_cast<T *>(A.y) + first * A.y_stride + (long long)h * A.V + col;
+    // lanes 0-11 of the first warp bring the lines of tokens further ahead into L2: 4 pieces of k and of
+    // q, 2 of v, a and beta
+    const char *ahead = nullptr;
+    long long ahead_step = 0;
+    if (warp == 0 && lane < 12) {
+        const int part = lane < 8 ? lane >> 2 : lane < 10 ? 2 : lane - 7, piece = lane < 8 ? lane & 3 : lane & 1;
+        const long long width = part < 2 ? KDIM / 4 : A.VS / 2;
+        ahead_step = (part == 0 ? A.k_stride : part == 1 ? A.q_stride : part == 2 ? A.v_stride : A.H) *
+                     (part < 3 ? (long long)sizeof(T) : 4);
+        ahead = part < 2 ? (const char *)(part ? A.q : A.k) + (hq * KDIM + piece * width) * sizeof(T)
+                : part == 2 ? (const char *)A.v + ((long long)h * A.V + slab * A.VS + piece * width) * sizeof(T)
+                            : (const char *)((part == 3 ? A.a : A.beta) + h);
+        ahead += (first + DELTA_AHEAD) * ahead_step;
+    }
     for (int t = 0; t < len; ++t, y += A.y_stride) {
         const DeltaToken<T> c = x;
         if (t + 1 < len) delta_load<T>(A, first + t + 1, h, hq, ks, col, x);
+        if (ahead && t + DELTA_AHEAD < len) asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead));
+        ahead += ahead_step;
         delta_token<T>(A, c, s, y);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) st4(Sg + (long long)(32 * (i >> 2) + (i & 3)) * A.V, s[i]);
+    for (int i = 0; i < 8; ++i) {
+        float *r = Sg + (long long)(32 * (i >> 1) + 2 * (i & 1)) * A.V;
+        st4(r, make_float4(s[i][0].x, s[i][1].x, s[i][2].x, s[i][3].x));
+        st4(r + A.V, make_float4(s[i][0].y, s[i][1].y, s[i][2].y, s[i][3].y));
+    }
 }
 
 // Single tokens of many rows: the states are all that counts, so the kernel is a stream of them.
@@ -374,7 +439,9 @@ cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
     // 4: 7.0, 5.2; 128: 143, 94).  Wider states would be streamed by slabs, a copy for each of their
     // rows: 320 states of 256 columns took 34 us that way, 28 by the first kernel.
     if (a.cu || a.V > DS_VW || 2 * states <= sms) {
-        delta_kernel<T><<<(unsigned)(states * (a.V / a.VS)), 2 * a.VS, 0, stream>>>(a);
+        DeltaArgs A = a;
+        A.sort = a.cu && a.rows > 1 && a.rows <= DELTA_SORT && states * (a.V / a.VS) > sms;
+        delta_kernel<T><<<(unsigned)(states * (a.V / a.VS)), 2 * a.VS, 0, stream>>>(A);
     } else {
         const size_t smem = (sizeof(DsSmem) + 127) / 128 * 128 + (size_t)DS_STAGES * KDIM * a.V * 4;
         cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

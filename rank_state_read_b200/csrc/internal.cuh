@@ -132,6 +132,7 @@ struct DeltaArgs {
     void *y;
     int *status;
     long long wait_limit;
+    int sort;    // the token-by-token kernel takes the longest sequences first
     int polls;   // the chunk kernel's wait limit in polls
     int before;  // its sequences that earlier launches of the call take (cu and slot point behind them)
 };

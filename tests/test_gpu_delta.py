@@ -633,3 +633,44 @@ def test_what_is_not_finite_stays_in_its_sequence(dtype, bad):
     for i in sick[1:]:
         first = c.cu[i] + lens[i] // 2 // 64 * 64
         assert bool(torch.isfinite(got[1][0][c.cu[i]:first].float()).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [41, 63, 64, 65])
+def test_sequences_taken_longest_first(dtype, n):
+    """Short sequences, many of them of one length or empty, on more CTAs than there are SMs; a slot out
+    of range, one named twice, bounds out of order, and padding with any bounds among them."""
+    import torch
+    import rank_state_read_b200 as rs
+    g = np.random.default_rng(26)
+    lens = [int(x) for x in g.integers(0, 8, n)]
+    lens[2], lens[30], lens[7], lens[33], lens[n - 2], lens[n - 1] = 40, 40, 3, 3, 0, 0
+    slot = g.permutation(n).tolist()
+    slot[n - 2] = slot[n - 1] = -1
+    assert sum(lens) <= 10 * n
+    c = Case(lens, n, 5, 5, 144, dtype, slot=slot, seed=26, behind=2)
+    c.slot_d[7] = n
+    c.slot_d[33] = slot[2]
+    c.cu_d[n - 1:] = torch.tensor([-(1 << 31), (1 << 31) - 1], dtype=torch.int32)
+    c.cu_d[n - 2] = c.cu[n - 2] + 2**20
+    bad_last = c.slot[n - 3]  # its end lies far behind the tokens
+    run_chunk(c)
+    with pytest.raises(rs.SketchSSMError):
+        c.plan.check()
+    c.slot[7] = c.slot[33] = c.slot[n - 3] = -1
+    assert bad_last >= 0
+    c.check()
+
+
+def test_one_short_sequence_either_way():
+    """A single sequence of up to 20 tokens and one of 21 go different ways: the first 20 tokens of both
+    have the same outputs, within twice what each may be off."""
+    import rank_state_read_b200 as rs
+    a = Case([20], 1, 4, 2, 128, "float16", seed=27, behind=1)
+    b = Case([21], 1, 4, 2, 128, "float16", seed=27)
+    for c in (a, b):
+        rs.sketchssm_delta_chunk(c.plan, c.cu_d, *c.args())
+        c.check()
+    top = float(b.dev["S"].norm(dim=2).max())
+    off = (a.dev["y"][:20].double() - b.dev["y"][:20].double()).abs() - 2 * b.eps * a.dev["y"][:20].double().abs()
+    assert float(off.max()) <= 4 * state_tol(21) * max(top, 3.0)
