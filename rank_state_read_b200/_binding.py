@@ -347,6 +347,13 @@ def _rows3(t, name: str, dtype, shape):
     return t.data_ptr(), s0
 
 
+def _count(n: int) -> int:
+    """A number of rows or tokens, which the C interface takes in 32 bits."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{n} rows are more than a call takes")
+    return n
+
+
 def _ints(t, name: str, numel: int):
     if t is None:
         return None
@@ -384,7 +391,7 @@ def sketchssm_delta_chunk(plan: Plan, cu, q, k, v, a, beta, S, y, *, slot=None, 
         raise TypeError("cu must be an int32 CUDA tensor of one entry more than there are sequences")
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    n, seqs = q.shape[0], cu.numel() - 1
+    n, seqs = _count(q.shape[0]), _count(cu.numel() - 1)
     td, ptrs = _delta(plan, n, q, k, v, a, beta, S, y, normalize_qk, scale)
     _check(load().sketchssm_delta_chunk(plan.handle, td, seqs, n, _ints(cu, "cu", seqs + 1),
                                         _ints(slot, "slot", seqs), *ptrs, _stream(stream)), "sketchssm_delta_chunk")
@@ -396,7 +403,7 @@ def sketchssm_delta_step(plan: Plan, q, k, v, a, beta, S, y, *, slot=None, norma
     state i).  Tensors as for sketchssm_delta_chunk."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    n = q.shape[0]
+    n = _count(q.shape[0])
     td, ptrs = _delta(plan, n, q, k, v, a, beta, S, y, normalize_qk, scale)
     _check(load().sketchssm_delta_step(plan.handle, td, n, _ints(slot, "slot", n), *ptrs, _stream(stream)),
            "sketchssm_delta_step")
@@ -415,6 +422,7 @@ def sketchssm_gated_norm(x, z, weight, out, *, eps: float = 1e-6, activation: st
     if activation not in GATES:
         raise ValueError(f"activation must be one of {sorted(GATES)}, got {activation!r}")
     n, groups, width = shape = x.shape
+    _count(max(n, groups, width))
     xp, xs = _rows3(x, "x", x.dtype, shape)
     zp, zs = (None, 0) if z is None else _rows3(z, "z", out.dtype, shape)
     op, os_ = _rows3(out, "out", out.dtype, shape)

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaAr
     // q, 2 of v, a and beta
     const char *ahead = nullptr;
     long long ahead_step = 0;
-    if (warp == 0 && lane < 12) {
+    if (len > DELTA_AHEAD && warp == 0 && lane < 12) {
         const int part = lane < 8 ? lane >> 2 : lane < 10 ? 2 : lane - 7, piece = lane < 8 ? lane & 3 : lane & 1;
         const long long width = part < 2 ? KDIM / 4 : A.VS / 2;
         ahead_step = (part == 0 ? A.k_stride : part == 1 ? A.q_stride : part == 2 ? A.v_stride : A.H) *

@@ -86,3 +86,16 @@ def test_norm_reference():
     assert np.allclose(norm_ref(x, z, w, 0.0, "sigmoid", False), [[[3 / r, 4 / r]]])
     assert np.allclose(norm_ref(x, z, w, 0.0, "silu", True), [[[0, np.sqrt(2)]]])
     assert np.allclose(norm_ref(x, None, w, 0.0, "silu", False), [[[6 / r, 4 / r]]])
+
+
+def test_binding_refuses_counts_past_32_bits():
+    import torch
+    for n in (2**31, 2**32 + 2):
+        x = torch.empty(n, 1, 128, device="meta", dtype=torch.bfloat16)
+        few = torch.empty(8, device="meta", dtype=torch.int32)
+        with pytest.raises(ValueError, match="more than a call takes"):
+            rs.sketchssm_gated_norm(x, x, torch.empty(128, device="meta"), x)
+        with pytest.raises(ValueError, match="more than a call takes"):
+            rs.sketchssm_delta_step(None, x, x, x, x, x, x, x)
+        with pytest.raises(ValueError, match="more than a call takes"):
+            rs.sketchssm_delta_chunk(None, few, x, x, x, x, x, x, x)
