@@ -22,11 +22,16 @@ def _dev(x, device) -> torch.Tensor:
 
 
 def _new(like: torch.Tensor, stream) -> torch.Tensor:
-    """A packed tensor of ``like``'s shape and type for work on ``stream``: its memory is not handed out
-    again before that work is done."""
-    t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    """A packed tensor of ``like``'s shape and type for work on ``stream``.  Its memory comes from that
+    stream's pool, so no other stream's work on it is pending, and is not handed out again before what
+    the current stream does with the tensor is done."""
+    if stream is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
