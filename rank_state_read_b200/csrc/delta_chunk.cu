@@ -49,6 +49,7 @@
 #include "dtype_util.cuh"
 #include "internal.cuh"
 #include "ptx_util.cuh"
+#include "wait_rule.cuh"
 
 namespace sk {
 namespace {
@@ -93,7 +94,7 @@ struct DcSmem {
     uint64_t b_ld[DC_KV], b_free[DC_KV], b_kq[DC_KV], b_v[2], b_vfree[2], b_sc[2], b_tp[2], b_out[2];
     uint64_t b_S, b_KS, b_QS, b_R, b_U, b_W, b_D, b_PU, b_KK, b_end;
     uint32_t taddr;
-    int stop;
+    int polls, late;                  // polls until a wait is late (negative: one has been given up); whether one was
     uint32_t dup[DC_MAX_SEQS / 32];
     uint16_t order[DC_MAX_SEQS];      // sequences, longest first
 };
@@ -329,7 +330,12 @@ __device__ __forceinline__ void dc_next(const DeltaArgs &A, const DcSmem &sm, Dc
 }
 
 // ---- waits: a number of polls of up to 20 us each; past the plan's limit recorded, past the
-// default limit given up, after which nothing waits any more and the kernel runs out ----
+// default limit given up.  Then no wait that begins polls any more (wait_rule.cuh): the roles go
+// through their chunks without waiting, no copies in or out are started and nothing is written to memory.
+// Before the CTA ends, its copies and products under way are waited for, with a limit again.  The limit
+// and the record lie in shared memory, and the plan's status word is told at the end: 48 prompts take
+// 922 us so, 939 with the word told in each wait, whose code counts; a look at a flag by every wait
+// costs 1% to 2% more. ----
 __device__ __forceinline__ bool dc_poll(uint64_t *bar, uint32_t parity)
 {
     uint32_t ok;
@@ -343,17 +349,28 @@ __device__ __forceinline__ bool dc_poll(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
+struct DcWaitOps {
+    const DeltaArgs &A;
+    DcSmem &sm;
+    uint64_t *bar;
+    uint32_t parity;
+    __device__ __forceinline__ int limit() const { return *(volatile int *)&sm.polls; }
+    __device__ __forceinline__ bool test() const { return mbar_test_wait(bar, parity); }
+    __device__ __forceinline__ bool poll() const { return dc_poll(bar, parity); }
+    __device__ __forceinline__ void late() const { *(volatile int *)&sm.late = 1; }
+    __device__ __forceinline__ void stop() const { *(volatile int *)&sm.polls = -1; }
+    __device__ __forceinline__ bool stopped() const { return limit() < 0; }
+};
+
 __device__ __forceinline__ void dc_wait(const DeltaArgs &A, DcSmem &sm, uint64_t *bar, uint32_t parity)
 {
-    if (mbar_test_wait(bar, parity)) return;
-    int left = A.polls;
-    do {
-        if (--left < 0) {
-            atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
-            if (left < -DC_MOST_POLLS) *(volatile int *)&sm.stop = 1;
-            if (*(volatile int *)&sm.stop) return;
-        }
-    } while (!dc_poll(bar, parity));
+    wait_by_rule(DcWaitOps{A, sm, bar, parity}, DC_MOST_POLLS);
+}
+
+// Whether a wait has been given up, the same for all lanes of the warp.
+__device__ __forceinline__ bool dc_stopped(const DcSmem &sm)
+{
+    return __any_sync(0xffffffffu, *(const volatile int *)&sm.polls < 0);
 }
 
 // one arrival for a warp whose lanes have all done their part
@@ -378,6 +395,7 @@ __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm, const D
 {
     const uint32_t leads = elect_lane();
     DcWalk w, ahead;
+    int nk = 0, nv = 0;  // chunks whose q and k, whose v were asked for
     dc_start(ahead);
     // q and k go one chunk before v: they are needed earlier, and v's place is free later
 #pragma unroll 1
@@ -387,6 +405,8 @@ __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm, const D
         if (ahead.there) {
             const int st = (n + 1) % DC_KV;
             if (n + 1 >= DC_KV) dc_wait(A, sm, &sm.b_free[st], ((n + 1) / DC_KV - 1) & 1);
+            if (dc_stopped(sm)) break;
+            ++nk;
             if (leads) {
                 const int x = ahead.h / A.hpq * KDIM, y = ahead.first + ahead.chunk * DC_C;
                 const uint32_t dst = smem_addr(sm.kq[st][0]);
@@ -403,12 +423,19 @@ __device__ __forceinline__ void dc_bring(const DeltaArgs &A, DcSmem &sm, const D
         if (!w.there) break;
         const int sv = n & 1;
         if (n >= 2) dc_wait(A, sm, &sm.b_vfree[sv], (n / 2 - 1) & 1);
+        if (dc_stopped(sm)) break;
+        ++nv;
         if (leads) {
             mbar_arrive_expect_tx(&sm.b_v[sv], 64 * 256);
             tma_load(smem_addr(sm.v[sv]), &maps.v, w.h * A.V + w.slice * DC_VW, w.first + w.chunk * DC_C, &sm.b_v[sv]);
         }
         __syncwarp();
     }
+    // each stage's last copies have landed before the CTA ends, read or not
+#pragma unroll 1
+    for (int c = max(nk - DC_KV, 0); c < nk; ++c) mbar_wait_bounded(&sm.b_ld[c % DC_KV], (c / DC_KV) & 1, DEFAULT_WAIT_CYCLES);
+#pragma unroll 1
+    for (int c = max(nv - 2, 0); c < nv; ++c) mbar_wait_bounded(&sm.b_v[c & 1], (c / 2) & 1, DEFAULT_WAIT_CYCLES);
 }
 
 // ---- outputs, from the place of their chunk's values ----
@@ -427,6 +454,7 @@ __device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm, const D
         const int sv = n & 1, t0 = w.first + w.chunk * DC_C;
         const int left = w.len - w.chunk * DC_C, cols = A.V - w.slice * DC_VW;
         dc_wait(A, sm, &sm.b_out[sv], (n / 2) & 1);
+        if (dc_stopped(sm)) break;
         if (left >= DC_C && cols >= DC_VW) {
             if (leads) {
                 asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&maps.y),
@@ -874,6 +902,7 @@ __device__ __forceinline__ void dc_prep(const DeltaArgs &A, DcSmem &sm, uint32_t
         warp_arrive(&sm.b_tp[tp]);
         named_sync(5, DC_PREP);  // T in fp32 has been read
     }
+    if (wq == 0 && leads) umma_commit(&sm.b_end);
 }
 
 // ---- the chain's products ----
@@ -945,10 +974,7 @@ __device__ __forceinline__ void dc_issue(const DeltaArgs &A, DcSmem &sm, uint32_
         }
         __syncwarp();
     }
-    if (*(volatile int *)&sm.stop) {  // a wait was given up: let what is in flight end before tensor memory goes
-        if (leads) umma_commit(&sm.b_end);
-        mbar_wait_bounded(&sm.b_end, 0, DEFAULT_WAIT_CYCLES);
-    }
+    if (leads) umma_commit(&sm.b_end);
 }
 
 // ---- the chain ----
@@ -1002,6 +1028,7 @@ __device__ __forceinline__ void dc_chain(const DeltaArgs &A, DcSmem &sm, uint32_
                     S[16 * b + i] = __ffma2_rn(two(sW), x[i], __fmul2_rn(gC, S[16 * b + i]));
             }
             if (w.chunk * DC_C + DC_C >= w.len) {
+                if (*(volatile int *)&sm.polls < 0) own = false;  // (in the store's condition: spills)
                 if (own) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -1181,7 +1208,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        sm.stop = 0;
+        sm.polls = A.polls;
+        sm.late = 0;
         for (int i = 0; i < DC_KV; ++i) {
             mbar_init(&sm.b_ld[i], 1);
             mbar_init(&sm.b_free[i], 1);
@@ -1197,7 +1225,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
         mbar_init(&sm.b_S, DC_CHAIN / 32);
         mbar_init(&sm.b_R, DC_CHAIN / 32);
         mbar_init(&sm.b_W, DC_CHAIN / 32);
-        for (uint64_t *b : {&sm.b_KS, &sm.b_QS, &sm.b_U, &sm.b_D, &sm.b_PU, &sm.b_KK, &sm.b_end}) mbar_init(b, 1);
+        for (uint64_t *b : {&sm.b_KS, &sm.b_QS, &sm.b_U, &sm.b_D, &sm.b_PU, &sm.b_KK}) mbar_init(b, 1);
+        mbar_init(&sm.b_end, 2);  // both warps that issue products, when their last ones are done
         mbar_fence_init();
     }
     // what stays zero: T and P right of column 32 in rows below 32, A there
@@ -1230,7 +1259,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1) delta_chunk_kernel(const DeltaA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(sm.taddr, 512);
+    if (threadIdx.x == 0 && sm.late) atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
+    if (warp == 0) {
+        mbar_wait_bounded(&sm.b_end, 0, DEFAULT_WAIT_CYCLES);
+        __syncwarp();
+        tmem_dealloc(sm.taddr, 512);
+    }
 }
 
 // a map of a token tensor's 64-row, `box`-column tiles
