@@ -22,6 +22,7 @@
 #include "dtype_util.cuh"
 #include "internal.cuh"
 #include "ptx_util.cuh"
+#include "wait_rule.cuh"
 
 namespace sk {
 namespace {
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
     int row = -1;
     long long first = 0, slot = 0;
     bool good = false;
+    RingPhases ring;
     auto bring = [&](int i) {
         const int st = (i - from) % DS_STAGES;
         const int r = i / A.H, h = i - r * A.H;
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
             row = r;
             good = delta_row(A, row, first, len, slot);
         }
+        if (good) ring.issued(st);
         if (warp == 0) {
             if (lane == 0) {
                 sm.slot[st] = good ? (int)slot : -1;
@@ -334,7 +337,6 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
     for (int i = from; i < from + DS_STAGES && i < to; ++i) bring(i);
     __syncthreads();
 
-    uint32_t phase = 0;  // parity of each stage's next copy
     for (int i = from; i < to; ++i) {
         const int st = (i - from) % DS_STAGES, pb = (i - from) & 1;
         const int h = i % A.H, col = 4 * lane;
@@ -357,11 +359,11 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
             kk = warp_sum(dot4(k4, k4));
             qq = warp_sum(dot4(q4, q4));
             qk = warp_sum(dot4(q4, k4));
-            if (!mbar_wait_bounded(&sm.full[st], phase >> st & 1, A.wait_limit)) {
+            if (!mbar_wait_bounded(&sm.full[st], ring.parity(st), A.wait_limit)) {
                 atomicOr(A.status, SK_STATUS_DELTA_TIMEOUT);
-                lost = !mbar_wait_bounded(&sm.full[st], phase >> st & 1, DEFAULT_WAIT_CYCLES);
+                lost = !mbar_wait_bounded(&sm.full[st], ring.parity(st), DEFAULT_WAIT_CYCLES);
             }
-            phase ^= 1u << st;
+            if (!lost) ring.landed(st);
             const float *src = states + (size_t)st * KDIM * V + r0 * V + 4 * lane;
             float4 d = zero4(), p = zero4();
             if (on) {
@@ -382,9 +384,11 @@ __global__ void __launch_bounds__(DS_THREADS, 1) delta_step_kernel(const DeltaAr
             }
         }
         if (__syncthreads_or(lost)) {
-            // given up: let the copies still on their way land (bounded) before the CTA exits
+            // given up: let the copies still on their way, the lost one among them, land (bounded)
+            // before the CTA exits
             if (threadIdx.x == 0)
-                for (int j = 0; j < DS_STAGES; ++j) mbar_wait_bounded(&sm.full[j], phase >> j & 1, DEFAULT_WAIT_CYCLES);
+                for (int j = 0; j < DS_STAGES; ++j)
+                    if (ring.pending(j)) mbar_wait_bounded(&sm.full[j], ring.parity(j), DEFAULT_WAIT_CYCLES);
             __syncthreads();
             return;
         }

@@ -1,5 +1,5 @@
-// When a wait inside a kernel is recorded and when it is given up.  No device calls, so that a host
-// program can run it.
+// When a wait inside a kernel is recorded and when it is given up, and which copies are under way then.
+// No device calls, so that a host program can run it.
 #pragma once
 
 #ifdef __CUDACC__
@@ -30,5 +30,21 @@ SK_HD bool wait_by_rule(Ops &&ops, int most)
     } while (!ops.poll());
     return true;
 }
+
+// Phases of a ring of up to 16 stages that one copy after another fills: which parity the next wait on a
+// stage takes, and which stages have a copy under way.  A wait that was lost leaves both as they are,
+// so that a later one still asks for that copy.
+struct RingPhases {
+    unsigned parity_bits = 0, under_way = 0;
+
+    SK_HD void issued(int stage) { under_way |= 1u << stage; }
+    SK_HD unsigned parity(int stage) const { return parity_bits >> stage & 1; }
+    SK_HD bool pending(int stage) const { return under_way >> stage & 1; }
+    SK_HD void landed(int stage)
+    {
+        parity_bits ^= 1u << stage;
+        under_way &= ~(1u << stage);
+    }
+};
 
 }  // namespace sk

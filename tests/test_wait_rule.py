@@ -1,5 +1,5 @@
-"""The rule by which a kernel's waits are recorded and given up (csrc/wait_rule.cuh), run on the host with
-phases that complete after so many polls, or never."""
+"""The rule by which a kernel's waits are recorded and given up, and the account of a ring's copies
+(csrc/wait_rule.cuh), run on the host with phases that complete after so many polls, or never."""
 from __future__ import annotations
 
 import subprocess
@@ -61,6 +61,47 @@ int main()
 }
 """
 
+RING = r"""
+#include <random>
+// barriers as the hardware counts them: `done` completed phases a stage, a test of parity p succeeds when the
+// phase that is open has the other one
+int main()
+{
+    std::mt19937 g(1);
+    for (int run = 0; run < 20000; ++run) {
+        const int stages = 1 + g() % 5, items = 1 + g() % 20, lose = g() % (items + 1);
+        sk::RingPhases r;
+        int done[16] = {}, out[16] = {};  // completed phases, copies asked for
+        bool skipped[64];
+        for (int i = 0; i < items; ++i) skipped[i] = g() % 4 == 0;  // rows to leave alone bring nothing
+        auto bring = [&](int i) { if (!skipped[i]) { r.issued(i % stages); ++out[i % stages]; } };
+        auto test = [&](int st) { return (unsigned)(done[st] & 1) != r.parity(st); };
+        for (int i = 0; i < stages && i < items; ++i) bring(i);
+        for (int i = 0; i < items; ++i) {
+            const int st = i % stages;
+            if (!skipped[i]) {
+                CHECK(r.pending(st) && !test(st));  // it has not landed: a wait waits
+                if (i == lose) break;               // given up: neither landed() nor the next copy
+                ++done[st];
+                CHECK(test(st));
+                r.landed(st);
+            }
+            if (i + stages < items) bring(i + stages);
+        }
+        // what is under way is what was asked for and has not landed, and a wait for it waits for that copy
+        for (int st = 0; st < stages; ++st) {
+            CHECK(r.pending(st) == (out[st] > done[st]) && out[st] - done[st] <= 1);
+            if (r.pending(st)) {
+                CHECK(!test(st));
+                ++done[st];
+                CHECK(test(st));
+            }
+        }
+    }
+    return 0;
+}
+"""
+
 
 def run(tmp_path, source):
     src, exe = tmp_path / "t.cpp", tmp_path / "t"
@@ -70,6 +111,6 @@ def run(tmp_path, source):
     assert r.returncode == 0, r.stdout
 
 
-@pytest.mark.parametrize("source", [WAITS], ids=["waits"])
+@pytest.mark.parametrize("source", [WAITS, RING], ids=["waits", "ring"])
 def test_rule(tmp_path, source):
     run(tmp_path, source)
