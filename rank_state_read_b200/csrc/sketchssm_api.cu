@@ -753,6 +753,9 @@ sketchssm_status row_span(long long &stride, long long elems, long long rows, in
     if (stride * size % 16 != 0)
         return fail(SKETCHSSM_ERR_ALIGNMENT, std::string(name) + " stride is not a multiple of 16 bytes");
     if (stride > (1LL << 36)) return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " stride is too large");
+    // (the bytes below must not wrap round 64 bits and look like few)
+    if (rows - 1 > (1LL << 46) / stride)
+        return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(name) + " spans more memory than there can be");
     *bytes = rows ? (size_t)((rows - 1) * stride + elems) * size : 0;
     return SKETCHSSM_OK;
 }

@@ -99,3 +99,18 @@ def test_binding_refuses_counts_past_32_bits():
             rs.sketchssm_delta_step(None, x, x, x, x, x, x, x)
         with pytest.raises(ValueError, match="more than a call takes"):
             rs.sketchssm_delta_chunk(None, few, x, x, x, x, x, x, x)
+
+
+def test_spans_past_64_bits_are_refused(lib):
+    """rows * stride may wrap round 64 bits; what is left then looks like a tensor of one row."""
+    text = lambda: lib.sketchssm_last_error().decode()
+    fake = ctypes.c_void_p(1 << 40)  # never read: the span is refused before any pointer is looked at
+    for stride, rows in ((1 << 36, (1 << 28) + 1), (1 << 36, (1 << 29) + 1), (1 << 36, (1 << 27) + 1), (1 << 35, (1 << 30) + 1),
+                         (1 << 36, 0x7FFFFFFF), (1 << 34, 0x7FFFFFFF), (128, 1 << 25)):
+        for field in ("x_stride", "z_stride", "out_stride"):
+            nd = rs.NormDesc(1, 1, 1, 128, 1, 0, 0, 1e-6, 0, 0, 0)
+            setattr(nd, field, stride)
+            status = lib.sketchssm_gated_norm(ctypes.byref(nd), rows, fake, fake, fake, fake, None)
+            assert status == 1, (stride, rows, field, status)
+            large = stride * (rows - 1) > 1 << 46
+            assert (f"{field[:-7]} spans" in text()) == large, (stride, rows, text())
