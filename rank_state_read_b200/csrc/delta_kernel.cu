@@ -447,8 +447,11 @@ cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
         A.sort = a.cu && a.rows > 1 && a.rows <= DELTA_SORT && states * (a.V / a.VS) > sms;
         delta_kernel<T><<<(unsigned)(states * (a.V / a.VS)), 2 * a.VS, 0, stream>>>(A);
     } else {
-        const size_t smem = (sizeof(DsSmem) + 127) / 128 * 128 + (size_t)DS_STAGES * KDIM * a.V * 4;
-        cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const size_t head = (sizeof(DsSmem) + 127) / 128 * 128, column = (size_t)DS_STAGES * KDIM * 4;
+        const size_t smem = head + column * a.V;
+        // the limit belongs to the function, which other threads launch for other sizes: always the largest
+        cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(head + column * DS_VW));
         if (e != cudaSuccess) return e;
         delta_step_kernel<T><<<(unsigned)(states < sms ? states : sms), DS_THREADS, smem, stream>>>(a);
     }

@@ -674,3 +674,35 @@ def test_one_short_sequence_either_way():
     top = float(b.dev["S"].norm(dim=2).max())
     off = (a.dev["y"][:20].double() - b.dev["y"][:20].double()).abs() - 2 * b.eps * a.dev["y"][:20].double().abs()
     assert float(off.max()) <= 4 * state_tol(21) * max(top, 3.0)
+
+
+def test_threads_with_states_of_different_size():
+    """Layers whose states differ in width, stepped from several threads through the C entry: no call
+    changes what another's launch needs."""
+    import ctypes
+    import threading
+
+    import torch
+    import rank_state_read_b200 as rs
+    lib, td = rs.load(), rs.TokenDesc(1, 0, 1.0, 0, 0, 0, 0)
+    cases = [Case([1] * 40, 40, 4, 2, V, "bfloat16", seed=28) for V in (128, 16) * 4]
+    streams = [torch.cuda.Stream() for _ in cases]
+    bad = []
+    start = threading.Barrier(len(cases))
+    torch.cuda.synchronize()
+
+    def work(c, st):
+        args = [c.plan.handle, ctypes.byref(td), 40, None, *(t.data_ptr() for t in c.args()), st.cuda_stream]
+        start.wait()
+        for _ in range(5000):
+            status = lib.sketchssm_delta_step(*args)
+            if status:
+                bad.append((status, lib.sketchssm_last_error()))
+                return
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
