@@ -358,8 +358,9 @@ typedef struct {
  *    window and buffers are not used.  A sketch is formed with sketchssm_flush(n_tokens = 0)
  *    afterwards; that leaves the sketches of other rows what they were.
  *  - cu [seqs+1] and slot [seqs] are int32 on the device; slot NULL: sequence i has state i
- *    (then seqs <= B).  a, beta [tokens][H] fp32, a in [0, 1].  q, k, v, y as td says; y
- *    overlaps no input.
+ *    (then seqs <= B).  a, beta [tokens][H] fp32, a in [0, 1].  q, k, v, y as td says; y and S
+ *    share no memory with another tensor (else SKETCHSSM_ERR_INVALID_ARG), though rows of
+ *    strided tensors may lie between one another.
  *  - An empty sequence, or one whose slot is negative (padding), is skipped: its state and
  *    its rows of y stay as they were, as do rows of y that no sequence holds.
  *  - Slots differ.  A sequence whose slot is >= B or is named by an earlier one too, or
@@ -411,7 +412,8 @@ typedef struct {
  * times the fp32 weight and the gate of z.  Gated DeltaNet: groups = H, width = V, the gate
  * after the norm; Mamba-2: groups = G, width = H V / G, the gate first, a weight a group.
  * z NULL: no gate.  Sums and products are fp32, out is rounded once.  out may be x or z
- * themselves where type and stride agree, and overlaps them in no other way.
+ * themselves where type and stride agree; it shares memory with x, z and weight in no other
+ * way (else SKETCHSSM_ERR_INVALID_ARG).
  */
 sketchssm_status sketchssm_gated_norm(const sketchssm_norm_desc *nd, int32_t rows, const void *x, const void *z,
                                       const float *weight, void *out, sketchssm_stream stream);

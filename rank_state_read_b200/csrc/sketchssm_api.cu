@@ -760,6 +760,40 @@ sketchssm_status row_span(long long &stride, long long elems, long long rows, in
     return SKETCHSSM_OK;
 }
 
+// The memory of a tensor: `rows` rows of `bytes` bytes, `stride` bytes apart (at least `bytes`).
+struct Span {
+    uintptr_t at;
+    size_t bytes, stride;
+    long long rows;
+
+    Span(const void *p, size_t bytes_, size_t stride_ = 0, long long rows_ = 1)
+        : at(reinterpret_cast<uintptr_t>(p)), bytes(bytes_), stride(stride_), rows(p && bytes_ ? rows_ : 0)
+    {
+    }
+    uintptr_t end() const { return at + (rows - 1) * stride + bytes; }
+    // whether the bytes x .. x + n - 1 meet one of its rows
+    bool meets(uintptr_t x, size_t n) const
+    {
+        if (x < at) return x + n > at;
+        if (rows == 1) return x - at < bytes;
+        const size_t row = (x - at) / stride, rest = (x - at) % stride;
+        return (long long)row < rows && (rest < bytes || ((long long)row + 1 < rows && rest + n > stride));
+    }
+};
+
+// Whether two tensors share memory.  Rows may lie between one another (slices of one buffer): with one
+// stride for both, the first row of the one that starts later meets the other's or none does.
+bool overlap(const Span &a, const Span &b)
+{
+    if (a.rows == 0 || b.rows == 0 || a.end() <= b.at || b.end() <= a.at) return false;
+    if (a.rows > 1 && b.rows > 1 && a.stride == b.stride)
+        return a.at >= b.at ? b.meets(a.at, a.bytes) : a.meets(b.at, b.bytes);
+    const Span &few = a.rows < b.rows ? a : b, &many = a.rows < b.rows ? b : a;
+    for (long long r = 0; r < few.rows; ++r)
+        if (many.meets(few.at + r * few.stride, few.bytes)) return true;
+    return false;
+}
+
 // cu NULL: one token a row
 sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc *td, int32_t rows, int32_t tokens,
                             bool chunk, const int32_t *cu, const int32_t *slot, const void *q, const void *k,
@@ -796,6 +830,15 @@ sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc 
     if ((long long)rows * H * (V / A.VS) > 0x7fffffffLL)
         return fail(SKETCHSSM_ERR_UNSUPPORTED, "rows * heads too large for one launch");
     if (rows == 0 || tokens == 0) return SKETCHSSM_OK;
+    const size_t e = es;
+    const Span qs(q, Q * K * e, A.q_stride * e, N), ks(k, Q * K * e, A.k_stride * e, N),
+        vs(v, H * V * e, A.v_stride * e, N), ys(y, H * V * e, A.y_stride * e, N), as(a, fbytes(N, H)),
+        bs(beta, fbytes(N, H)), Ss(S, fbytes(B, H, K, V)), cs(chunk ? cu : nullptr, sizeof(int32_t) * ((size_t)rows + 1)),
+        ls(slot, sizeof(int32_t) * (size_t)rows);
+    for (const Span *in : {&qs, &ks, &vs, &as, &bs, &cs, &ls})
+        if (overlap(ys, *in) || overlap(Ss, *in))
+            return fail(SKETCHSSM_ERR_INVALID_ARG, std::string(overlap(ys, *in) ? "y" : "S") + " overlaps an input");
+    if (overlap(ys, Ss)) return fail(SKETCHSSM_ERR_INVALID_ARG, "y overlaps S");
     if (chunk) CHECK_I(cu, sizeof(int32_t) * ((size_t)rows + 1), "cu", false);
     CHECK_I(slot, sizeof(int32_t) * (size_t)rows, "slot", true);
     CHECK_T(q, qb, "q", false);
@@ -826,9 +869,9 @@ sketchssm_status delta_impl(const sketchssm_plan *p, const sketchssm_token_desc 
     A.y = y;
     A.status = p->d_status;
     A.wait_limit = p->wait_limit;
-    cudaError_t e = sk::delta_chunk_fits(A) ? sk::launch_delta_chunk(A, p->sms, (cudaStream_t)stream)
+    const cudaError_t err = sk::delta_chunk_fits(A) ? sk::launch_delta_chunk(A, p->sms, (cudaStream_t)stream)
                                             : sk::launch_delta(A, p->sms, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_fail(e, "delta rule kernel launch");
+    if (err != cudaSuccess) return cuda_fail(err, "delta rule kernel launch");
     return SKETCHSSM_OK;
 }
 
@@ -882,6 +925,15 @@ extern "C" sketchssm_status sketchssm_gated_norm(const sketchssm_norm_desc *nd, 
     A.items = (long long)rows * nd->groups;
     if (A.items > 0x7fffffffLL) return fail(SKETCHSSM_ERR_UNSUPPORTED, "rows * groups too large for one launch");
     if (rows == 0) return SKETCHSSM_OK;
+    const size_t xe = dtype_size(nd->x_dtype), ze = dtype_size(nd->dtype);
+    const Span xs(x, elems * xe, A.x_stride * xe, rows), zs(z, elems * ze, A.z_stride * ze, rows),
+        os(out, elems * ze, A.out_stride * ze, rows), ws(weight, fbytes(nd->weight_groups, nd->width));
+    for (const Span *in : {&xs, &zs}) {
+        const bool itself = in->at == os.at && in->bytes == os.bytes && (rows == 1 || in->stride == os.stride);
+        if (!itself && overlap(os, *in))
+            return fail(SKETCHSSM_ERR_INVALID_ARG, std::string("out overlaps ") + (in == &xs ? "x" : "z") + " but is not the same tensor");
+    }
+    if (overlap(os, ws)) return fail(SKETCHSSM_ERR_INVALID_ARG, "out overlaps weight");
     CHECK_T(x, xb, "x", false);
     CHECK_T(z, zb, "z", true);
     CHECK_T(weight, fbytes(nd->weight_groups, nd->width), "weight", false);

@@ -706,3 +706,48 @@ def test_threads_with_states_of_different_size():
         t.join()
     torch.cuda.synchronize()
     assert not bad, bad
+
+
+@pytest.mark.parametrize("chunk", [True, False])
+def test_outputs_that_share_memory_are_refused(chunk):
+    import torch
+    import rank_state_read_b200 as rs
+    n, H = 6, 2
+    c = Case([4, 2] if chunk else [1] * n, 2 if chunk else n, H, H, K, "bfloat16", seed=29)
+    q, k, v, a, beta, S, y = c.args()
+    before = [t.clone() for t in c.args()]
+
+    def call(**kw):
+        args = [kw.get(m, t) for m, t in zip(("q", "k", "v", "a", "beta", "S", "y"), c.args())]
+        slot = kw.get("slot", c.slot_d)
+        if chunk:
+            rs.sketchssm_delta_chunk(c.plan, kw.get("cu", c.cu_d), *args, slot=slot)
+        else:
+            rs.sketchssm_delta_step(c.plan, *args, slot=slot)
+
+    buf = torch.zeros(4 * n * H * K, device="cuda", dtype=torch.bfloat16)
+    off = buf[K:K + n * H * K].view(n, H, K)             # the same rows, half a row on
+    wide = torch.zeros(n, 4 * H * K, device="cuda", dtype=torch.bfloat16)
+    part = lambda lo: wide[:, lo:lo + H * K].view(n, H, K)
+    flat = S.view(-1)
+    bad = [dict(y=q), dict(y=k), dict(y=v), dict(y=off, v=buf[:n * H * K].view(n, H, K)),
+           dict(y=part(K), q=part(2 * K)),                # columns that meet
+           dict(y=part(0), k=wide.view(-1)[3 * K:3 * K + n * H * K].view(n, H, K)),  # another stride
+           dict(y=flat[:n * H * K // 2].view(torch.bfloat16).view(n, H, K)),
+           dict(a=flat[:n * H].view(n, H)), dict(beta=flat[8:8 + n * H].view(n, H)),
+           dict(a=buf[:2 * n * H].view(torch.float32).view(n, H), y=buf[:n * H * K].view(n, H, K)),
+           dict(slot=flat[:c.slot_d.numel()].view(torch.int32))]
+    if chunk:
+        bad.append(dict(cu=flat[16:16 + c.cu_d.numel()].view(torch.int32)))
+    for kw in bad:
+        with pytest.raises(rs.SketchSSMError, match="overlaps") as e:
+            call(**kw)
+        assert e.value.status == 1, kw.keys()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, u) for t, u in zip(c.args(), before))
+    # rows of one buffer between one another: q | y | k | v
+    for lo, t in ((0, q), (2 * H * K, k), (3 * H * K, v)):
+        part(lo).copy_(t)
+    call(q=part(0), k=part(2 * H * K), v=part(3 * H * K), y=part(H * K))
+    y.copy_(part(H * K))
+    c.check()

@@ -114,3 +114,37 @@ def test_spans_past_64_bits_are_refused(lib):
             assert status == 1, (stride, rows, field, status)
             large = stride * (rows - 1) > 1 << 46
             assert (f"{field[:-7]} spans" in text()) == large, (stride, rows, text())
+
+
+def test_gated_norm_refuses_outputs_that_share_memory(lib):
+    """Against the bytes written out: out may be x or z, row for row, or lie between their rows."""
+    g = np.random.default_rng(3)
+    base = 1 << 40
+
+    def taken(at, row, stride, rows):
+        return np.concatenate([at + r * stride + np.arange(0, row, 16) for r in range(rows)])
+
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        rows, width = int(g.integers(1, 6)), 8 * int(g.integers(1, 4))
+        xt, t = int(g.integers(0, 3)), int(g.integers(0, 3))
+        xe, e = (4 if xt == 0 else 2), (4 if t == 0 else 2)
+        es = (xe, e, e)
+        same = 16 * int(g.integers(width // 4, width // 4 + 8))  # bytes
+        strides = [same if g.random() < 0.5 else width * s + 16 * int(g.integers(0, 6)) for s in es]
+        at = [base + 16 * int(g.integers(0, 40)) for _ in es]
+        if g.random() < 0.3:
+            at[2] = at[int(g.integers(0, 2))]
+        weight = base + 16 * int(g.integers(0, 60))
+        nd = rs.NormDesc(xt, t, 1, width, 1, 0, 0, 1e-6, *(b // s for b, s in zip(strides, es)))
+        out = taken(at[2], width * e, strides[2], rows)
+        want = np.intersect1d(out, taken(weight, width * 4, 0, 1)).size > 0
+        for i in range(2):
+            itself = at[i] == at[2] and es[i] == e and (rows == 1 or strides[i] == strides[2])
+            want = want or (not itself and np.intersect1d(out, taken(at[i], width * es[i], strides[i], rows)).size > 0)
+        p = [ctypes.c_void_p(a) for a in (at[0], at[1], weight, at[2])]
+        assert lib.sketchssm_gated_norm(ctypes.byref(nd), rows, *p, None) == 1  # none of them is device memory
+        found = "overlaps" in lib.sketchssm_last_error().decode()
+        assert found == want, (rows, width, xt, t, strides, at, weight, lib.sketchssm_last_error())
+        seen[want] += 1
+    assert min(seen.values()) > 500, seen
