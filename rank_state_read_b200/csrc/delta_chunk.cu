@@ -477,7 +477,15 @@ __device__ __forceinline__ void dc_store(const DeltaArgs &A, DcSmem &sm, const D
 
 // ---- the decays of a chunk's tokens, two tokens a lane ----
 
-__device__ __forceinline__ float pow2_of(long long d) { return ex2((float)d * 0x1p-40f); }  // 2^(d / 2^40)
+// 2^(d / 2^40), off by 2^-22 whatever the size of d: the whole part goes into the exponent as it is, and
+// the rest, of half a unit at most, through ex2.  (d rounded to fp32 as a whole is off by 2^-18 near
+// 100, and two tokens' factors of opposite exponents then make a decay off by up to 2^-17.5.)  Below
+// 2^-126: 0.
+__device__ __forceinline__ float pow2_of(long long d)
+{
+    const int whole = (int)((d + (1LL << 39)) >> 40), rest = (int)(d >> 8);  // rest / 2^32 in [-1/2, 1/2)
+    return ex2((float)rest * 0x1p-32f) * __uint_as_float((uint32_t)(min(max(whole, -127), 127) + 127) << 23);
+}
 
 __device__ __forceinline__ void dc_scalars(const DeltaArgs &A, DcSmem &sm)
 {
