@@ -28,27 +28,32 @@ __device__ __forceinline__ float gn_finite(float z)
     return r;
 }
 
-// Gates of two values.  By the hardware's exponential and reciprocal (a few 2^-22) where the result is
-// rounded to 16 bits, by expf and a division for fp32; in pairs, since at 128 columns of bf16 the
-// instructions bound the kernel next to HBM (162 us for 32768 x 32 x 128 element by element).
-template <bool FAST>
-__device__ __forceinline__ float2 gn_gate(float2 z, bool sigmoid)
+// Gate of one value, by expf and a division: exp(-|z|) stays in fp32's range, as exp(-z) does not below
+// -88.7, and leaves its normal numbers where the result does.
+__device__ __forceinline__ float gn_gate(float z, bool sigmoid)
 {
-    float2 s;
-    if (FAST) {
-        const float2 e = __fmul2_rn(z, make_float2(-1.44269504f, -1.44269504f));
-        float2 x;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.x) : "f"(e.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.y) : "f"(e.y));
-        x = __fadd2_rn(x, make_float2(1.f, 1.f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(x.x));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(x.y));
-    } else {
-        s = make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
-    }
-    if (sigmoid) return s;
-    // silu(-inf) = 0, not -inf * 0
-    return __fmul2_rn(make_float2(gn_finite(z.x), gn_finite(z.y)), s);
+    const float t = expf(-fabsf(z)), s = (z < 0.f ? t : 1.f) / (1.f + t);
+    return sigmoid ? s : gn_finite(z) * s;  // silu(-inf) = 0, not -inf * 0
+}
+
+// Gates of two values.  Where the result is rounded to 16 bits, by the hardware's exponential and
+// reciprocal (a few 2^-22), in pairs, since at 128 columns of bf16 the instructions bound the kernel next
+// to HBM (162 us for 32768 x 32 x 128 element by element).  The value and the exponential are scaled by
+// 2^-8 there (140 instead of 138 us): the reciprocal then stays a normal number down to z = -92.9, and
+// SiLU is one down to -91.9.
+template <bool FAST>
+__device__ __forceinline__ float2 gn_gates(float2 z, bool sigmoid)
+{
+    if (!FAST) return make_float2(gn_gate(z.x, sigmoid), gn_gate(z.y, sigmoid));
+    const float2 scale = make_float2(0x1p-8f, 0x1p-8f);
+    const float2 e = __ffma2_rn(z, make_float2(-1.44269504f, -1.44269504f), make_float2(-8.f, -8.f));
+    float2 x, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.y) : "f"(e.y));
+    x = __fadd2_rn(x, scale);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(x.y));
+    return __fmul2_rn(sigmoid ? scale : __fmul2_rn(make_float2(gn_finite(z.x), gn_finite(z.y)), scale), s);
 }
 
 // VECS vectors of 8 values a lane; LANES lanes (a power of two up to 32) or, with
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(GN_THREADS) gated_norm_kernel(const NormArgs A
 #pragma unroll
             for (int i = 0; i < VECS; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) g[i][e] = gn_gate<sizeof(T) == 2>(g[i][e], sigmoid);
+                for (int e = 0; e < 4; ++e) g[i][e] = gn_gates<sizeof(T) == 2>(g[i][e], sigmoid);
         };
         if (!A.z) {
 #pragma unroll

@@ -240,3 +240,28 @@ def test_layer_calls_on_another_stream():
         got.append((out, layer.S, layer.Y))
         layer.plan.check()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("t", ["bfloat16", "float32"])
+@pytest.mark.parametrize("activation", ["silu", "sigmoid"])
+@pytest.mark.parametrize("gate_first", [False, True])
+def test_gates_next_to_nothing(t, activation, gate_first):
+    """exp(-z) passes fp32's range at z = -88.7 and its reciprocal leaves the normal numbers at -87.3;
+    z / (1 + exp(-z)) is one down to -91.9, and a weight brings results back from below."""
+    import torch
+    import rank_state_read_b200 as rs
+    z = torch.linspace(-91.75, -80, 48, device="cuda").to(getattr(torch, t)).view(1, 6, 8).contiguous()
+    x = torch.ones(1, 6, 8, device="cuda", dtype=z.dtype) * (2.0 ** 64 if gate_first else 1.0)
+    w = torch.full((8,), 2.0 ** 30, device="cuda")
+    out = torch.empty_like(z)
+    eps = 1e-38 if gate_first else 1e-6
+    rs.sketchssm_gated_norm(x, z, w, out, eps=eps, activation=activation, gate_first=gate_first)
+    zz = z.double().cpu().numpy()
+    ref = norm_ref(x.double().cpu().numpy(), zz, w.double().cpu().numpy(), eps, activation, gate_first)
+    # the exponent z log2(e), up to 133, is off by 2^-17 before it is raised (relative 2^-17.5), or a
+    # subnormal gate by half a step of 2^-149 (2^-17.6 of exp(-91.75)); a group's root takes as much on
+    # again; then the rounding to the type
+    tol = 2.0 ** -16.5 + torch.finfo(z.dtype).eps / 2
+    low = 2.0 ** -149 * 2.0 ** 30
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= tol * np.abs(ref) + (low if not gate_first else 0)), got / ref
