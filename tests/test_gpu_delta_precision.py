@@ -5,7 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from delta_ref import K
+from delta_ref import delta_ref
 from test_gpu_delta import Case, run_chunk
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +51,45 @@ def test_decays_far_from_a_chunk_s_middle(dtype):
     left = np.abs(c.dev["S"][0, :, 31].double().cpu().numpy()).max(1)
     found = (c.host["a"][63][:, None] * np.abs(c.host["v"][62])).max(1)
     assert np.all(left <= 16.5 * 2.0 ** -23 * found), (left / found).max()
+
+
+# A chunk's roundings, as they reach the state: sums in fp32 of 16 (K S), 12 (T R) and 8 (the increment)
+# accumulations, which the tensor cores cut off, 2^-24 in the mean of each partial sum; the products
+# A holds two factors of 2^-22 of a decay, the state's increment one: 12 * 2^-24.  The pairs' 2^-22 and the
+# other roundings are spread to both sides, and disappear beside these in a 2-norm over 128 x V values.
+# A low part that is left out costs 2^-12 a value: 3e-6 (S, a chunk of 64 tokens) to 2e-4 (R) of the state.
+STATE = 48 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("lens", [[21], [64], [65], [200], [130, 64, 33]], ids=str)
+@pytest.mark.parametrize("decays", ["weak", "half", "strong"])
+def test_state_and_outputs_to_their_last_bits(dtype, lens, decays):
+    """The state in the 2-norm of each sequence and head; the outputs against the exact ones rounded to
+    their type.  Two roundings of values that are apart by d of a step differ in d of the cases, by a step
+    each: the sum of squares is then d * step^2, at most STATE * eps * |y|^2, since a step is at most
+    eps |y|.  One step of the largest value is allowed beside it, where few values make up the mean."""
+    import torch
+    H, V = 8, 128
+
+    def change(x):
+        g = np.random.default_rng(31)
+        if decays == "half":
+            x["a"][:] = g.uniform(0.4, 0.6, x["a"].shape)
+        if decays == "strong":  # more than 100 powers of two in a chunk
+            x["a"][:] = np.exp2(-g.exponential(5.0, x["a"].shape))
+    c = Case(lens, len(lens), H, 4, V, dtype, seed=31, change=change)
+    run_chunk(c)
+    c.plan.check()
+    torch.cuda.synchronize()
+    h = c.host
+    y, S, _ = delta_ref(c.cu, c.slot, h["q"], h["k"], h["v"], h["a"], h["beta"], h["S"])
+    got = c.dev["S"].double().cpu().numpy()
+    size = lambda t: np.sqrt((t * t).sum((2, 3)))
+    off = size(got - S) / size(S)
+    assert off.max() <= STATE, off.max()
+    eps = torch.finfo(c.dev["y"].dtype).eps
+    gy = c.dev["y"].double().cpu().numpy()
+    ry = torch.from_numpy(y).to(c.dev["y"].dtype).double().numpy()
+    limit = np.sqrt(STATE * eps) * np.linalg.norm(y) + eps * np.abs(y).max()
+    assert np.linalg.norm(gy - ry) <= limit, (np.linalg.norm(gy - ry) / np.linalg.norm(y), limit / np.linalg.norm(y))
