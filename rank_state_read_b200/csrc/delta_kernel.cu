@@ -257,10 +257,10 @@ __global__ void __launch_bounds__(DELTA_MAXVS * 2, 2) delta_kernel(const DeltaAr
 // up to 128 columns is one bulk copy, and three of them are on their way or in use, so that some
 // 128 KB a CTA are always in flight.  A warp has 16 rows of the state, a lane 4 columns of each:
 // every access is a run of whole lines.  512 rows of 32 heads of 128, bf16: 350 us,
-// 6.2 TB/s of states and tokens, 0.95 of the measured copy rate.  (The kernel
-// above takes 617 us for them, its layout with the next item's state loaded into registers 548 us; an
+// 6.2 TB/s of states and tokens, 0.94 of the measured copy rate.  (The kernel
+// above takes 556 us for them, its layout with the next item's state loaded into registers 548 us; an
 // item index in 64 bits, whose divisions every thread waits for, cost 45 us.)
-constexpr int DS_THREADS = 256, DS_STAGES = 3, DS_VW = 128;
+constexpr int DS_THREADS = 256, DS_STAGES = 3, DS_VW = 128, DS_LEAST_V = 64;
 
 struct DsSmem {
     float part[2][8][2][DS_VW];  // the warps' shares of k^T S and q^T S
@@ -438,11 +438,13 @@ template <class T>
 cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 {
     const long long states = (long long)a.rows * a.H;
-    // One token a row and states of up to 128 columns go through the stream of states, but for the
-    // fewest (32 heads of 128: one row 4.5 us by the first kernel, 4.9 by the stream; 2: 4.7, 4.9;
-    // 4: 7.0, 5.2; 128: 143, 94).  Wider states would be streamed by slabs, a copy for each of their
-    // rows: 320 states of 256 columns took 34 us that way, 28 by the first kernel.
-    if (a.cu || a.V > DS_VW || 2 * states <= sms) {
+    // One token a row and states of 64 to 128 columns go through the stream of states, but for the
+    // fewest.  First kernel / stream, us: 32 heads of 128, bf16: one row 4.4 / 4.9; 2: 4.6 / 4.9; 4: 6.9 /
+    // 5.1; 128: 141 / 95; 512: 556 / 350.  400 rows of 32 heads, by columns: 16: 62 / 188; 32: 113 / 191;
+    // 48: 161 / 197; 64: 220 / 210; 80: 314 / 225; 96: 315 / 242 (fp32 within 5%): below 64 columns half the
+    // stream's lanes idle.  Wider states would be streamed by slabs, a copy for each of their rows: 320
+    // states of 256 columns took 34 us that way, 28 by the first kernel.
+    if (a.cu || a.V < DS_LEAST_V || a.V > DS_VW || 2 * states <= sms) {
         DeltaArgs A = a;
         A.sort = a.cu && a.rows > 1 && a.rows <= DELTA_SORT && states * (a.V / a.VS) > sms;
         delta_kernel<T><<<(unsigned)(states * (a.V / a.VS)), 2 * a.VS, 0, stream>>>(A);

@@ -685,7 +685,7 @@ def test_threads_with_states_of_different_size():
     import torch
     import rank_state_read_b200 as rs
     lib, td = rs.load(), rs.TokenDesc(1, 0, 1.0, 0, 0, 0, 0)
-    cases = [Case([1] * 40, 40, 4, 2, V, "bfloat16", seed=28) for V in (128, 16) * 4]
+    cases = [Case([1] * 40, 40, 4, 2, V, "bfloat16", seed=28) for V in (128, 64) * 4]
     streams = [torch.cuda.Stream() for _ in cases]
     bad = []
     start = threading.Barrier(len(cases))
@@ -751,3 +751,20 @@ def test_outputs_that_share_memory_are_refused(chunk):
     call(q=part(0), k=part(2 * H * K), v=part(3 * H * K), y=part(H * K))
     y.copy_(part(H * K))
     c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [48, 64])
+def test_step_of_many_rows_of_narrow_states(dtype, V):
+    """The widest states that many rows take one by one, and the narrowest that are streamed."""
+    import rank_state_read_b200 as rs
+    rows = 90
+    slot = np.random.default_rng(32).permutation(rows + 3)[:rows].tolist()
+    slot[3] = slot[89] = -1
+    c = Case([1] * rows, rows + 3, 6, 2, V, dtype, slot=slot, seed=32, unit=False)
+    c.slot_d[50] = slot[7]
+    rs.sketchssm_delta_step(c.plan, *c.args(), slot=c.slot_d, normalize_qk=True, scale=0.5)
+    with pytest.raises(rs.SketchSSMError):
+        c.plan.check()
+    c.slot[50] = -1
+    c.check(normalize=True, scale=0.5)
