@@ -372,6 +372,9 @@ typedef struct {
  *  - A value that is infinite or no number reaches only its own sequence, in the heads that read
  *    it: the state and the outputs from its token on, and maybe those of up to 63 tokens before
  *    it, which are computed together with it.
+ *  - 16-bit prompts of more than 10 tokens a sequence on average (empty and padded ones counted;
+ *    one sequence: more than 20) are taken 64 tokens at a time, others token by token: a long
+ *    prompt among very many short or padded rows is faster in a call of its own.
  *  - seqs = 0 and tokens = 0 do nothing.  Nothing is allocated; the call can be captured
  *    into a graph.
  */

@@ -24,20 +24,22 @@
 //   warp 12     issues the chain's MMAs;
 //   warp 13     writes the outputs, 14 forms the decays, 15 brings q, k and v (tensor copies).
 //
-// Precision.  The state is held, and its errors count, in fp32.  Every operand x but q and k is
-// split into two fp16 parts, x = 2^-e (hi + lo) (1 + 2^-22), e from the largest value of its row
-// (or column), and products are taken hi hi + hi lo + lo hi in fp32; q and k, 8 or 11 bits wide,
-// are exact in fp16 after a row's power of two.  (fp16 pairs hold 22 bits where bf16 pairs hold
-// 16, and bf16 triples hold 24 for half as many products again.)  y is rounded once.
+// Precision.  The state is held in fp32, and after any prompt its error is 1e-7 to 3e-7 (2-norm of a head).
+// Every operand x but q and k is split into two fp16 parts, x = 2^-e (hi + lo) (1 + 2^-22), e from the
+// largest value of its row (or column), and products are taken hi hi + hi lo + lo hi in fp32; q and k, 8 or
+// 11 bits wide, go into fp16 after a row's power of two (bf16 values below 2^-31 of the row's largest
+// lose bits there).  Decays are off by 2^-22, products of two factors by twice that.  (fp16 pairs hold
+// 22 bits where bf16 pairs hold 16, and bf16 triples hold 24 for half as many products again.)  y is
+// rounded once.
 //
-// What bounds it.  The chain and the preparation each take some 9,700 SM cycles a chunk (of them
-// 2,560 of MMAs), and both wait for instructions more than for anything else: 2.5 of 6 stall
-// cycles an issued instruction.  A chunk runs some 60 KB of straight code in six roles,
-// where straight code beyond 32 KB came at 5.7 cycles an instruction and SM in
-// a loop of nothing else.  Loops in its place (re-reading tensor memory, or the triangular
-// products in one loop) traded that for latency and were slower at one sequence.  One sequence of
-// 8192 tokens, 32 heads of 128, bf16: 645 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
-// 263 us; 48 of 32768: 940 us, 4.8 times what HBM needs for the bytes.  Token by token: 4705, 1193
+// What bounds it.  A chunk takes 9,400 SM cycles (of them 2,560 of MMAs), 10,300 with all SMs at work.
+// The preparation sets that pace: it waits 600 of them, the chain waits 1,250 for it.  Both wait for
+// instructions more than for anything else: 2.4 of 6 stall cycles an issued instruction.  A chunk runs
+// some 60 KB of straight code in six roles, where straight code beyond 32 KB came at 5.7 cycles an
+// instruction and SM in a loop of nothing else.  Loops in its place (re-reading tensor memory, or the
+// triangular products in one loop) traded that for latency and were slower at one sequence.  One sequence
+// of 8192 tokens, 32 heads of 128, bf16: 638 us (32 of 148 SMs have work); 16 sequences of 8192 in all:
+// 259 us; 48 of 32768: 931 us, 4.7 times what HBM needs for the bytes.  Token by token: 4705, 1193
 // and 4339 us.  Slower were: 16 chain warps with half the work each (1044 us for the one sequence),
 // T by a warp group of its own (758), rows of q, k and v by bulk copies of 128 and 256 bytes (the copy
 // engine takes some 60 cycles a copy).
@@ -1329,7 +1331,9 @@ cudaError_t launch_type(const DeltaArgs &a, int sms, cudaStream_t stream)
 
 bool delta_chunk_fits(const DeltaArgs &a)
 {
-    // Sequences of up to 10 tokens on average, and a single one of up to 20, go token by token: 32
+    // Sequences of up to 10 tokens on average, and a single one of up to 20, go token by token (empty and
+    // padded ones count, since the host knows the bounds and slots of none; one prompt of 8192 tokens takes
+    // 639 us alone, 893 among 500 padded rows, 4810 among 1000): 32
     // heads of 128 columns, bf16, take (tokens a sequence: token by token / here) 10: 39 / 43 us for
     // 16 sequences, 563 / 553 for 256; 12: 43 / 43, 625 / 552; one sequence 10: 8.8 / 13.9, 20: 13.5 / 14.1,
     // 24: 15.1 / 14.1.

@@ -7,8 +7,10 @@
 // One pass: a group's values stay in registers between the sum of squares and the store,
 // so the kernel moves x, z and out once and is bound by HBM.  A group belongs to LANES
 // lanes (8 to 32, the width / 8 vectors of 8 values dealt out round robin), so that short
-// groups share a warp; groups of more than 512 values belong to a CTA.  Sums and
-// products are fp32; the only rounding to fewer bits is that of the stored value.
+// groups share a warp; groups of more than 512 values belong to a CTA.  Above 8192 values a thread has 64
+// of them, which spill in part.  Of the measured copy rate: 32768 x 32 x 128 bf16 0.88, 16384 x 32 x 128
+// fp32 0.96, 8192 groups of 16384 bf16 0.68, fp32 0.39.  Sums and products are fp32; the only rounding to
+// fewer bits is that of the stored value.
 #include <atomic>
 
 #include "device_util.cuh"
