@@ -106,3 +106,28 @@ def test_the_default_stream_by_its_handle(layer):
     want = run(None)
     got = run(torch.cuda.current_stream().cuda_stream)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("call", ["prompt", "prompt_gate", "step", "norm"])
+def test_captured_on_a_side_stream(layer, call):
+    """A call on a stream that a capture forked: its output belongs to the graph and is what replays give."""
+    import torch
+    run = calls(layer, 4)[call]
+    S0 = layer.S.clone()
+    want = run(None)[:2].clone()
+    S1 = layer.S.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()  # the copies are made before the other stream writes the state
+    run(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        out = run(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        layer.S.copy_(S0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:2], want) and torch.equal(layer.S, S1)
+    layer.plan.check()
